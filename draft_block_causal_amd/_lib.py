@@ -55,6 +55,12 @@ EXPORTED = [
     "domino_correction_backward_workspace_size",
     "domino_gru_backward",
     "domino_gru_backward_workspace_size",
+    "domino_quantize_rows",
+    "domino_base_logits_i8",
+    "domino_token_logprobs",
+    "domino_token_logprobs_workspace_size",
+    "domino_policy_loss",
+    "domino_policy_loss_workspace_size",
     "domino_debug_read_stream",
     "domino_debug_philox",
 ]
@@ -125,6 +131,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "domino_correction_backward_workspace_size": (ctypes.c_int, [HP, I32, ctypes.POINTER(SZ)]),
         "domino_gru_backward": (ctypes.c_int, [HP, I32, P, P, P, P, P, P, P, P, P, SZ, P]),
         "domino_gru_backward_workspace_size": (ctypes.c_int, [HP, I32, ctypes.POINTER(SZ)]),
+        "domino_quantize_rows": (ctypes.c_int, [I32, I32, I32, P, P, P, P]),
+        "domino_base_logits_i8": (ctypes.c_int, [I32, I32, I32, I32, P, P, P, P, P, P]),
+        "domino_token_logprobs": (ctypes.c_int, [I32, I32, I32, P, P, P, F, P, P, P, SZ, P]),
+        "domino_token_logprobs_workspace_size": (SZ, [I32, I32, I32]),
+        "domino_policy_loss": (ctypes.c_int, [I32, I32, I32, P, P, P, P, P, P, F, F, F, F, P, P, P, P, P, SZ, P]),
+        "domino_policy_loss_workspace_size": (SZ, [I32, I32, I32]),
         "domino_debug_read_stream": (ctypes.c_int, [P, SZ, P, P]),
         "domino_debug_philox": (ctypes.c_int, [U64, U32, I32, I32, I32, I32, P, P]),
     }
@@ -476,6 +488,164 @@ def domino_gru_backward(head: Head, x_t: torch.Tensor, teacher: torch.Tensor, gr
         head.ref, B, _ptr(x_t), _ptr(teacher), _ptr(gru_states), _ptr(d_states), _ptr(out["d_w_ih"]),
         _ptr(out["d_w_hh"]), _ptr(out["d_b_ih"]), _ptr(out["d_b_hh"]), _ptr(ws), ws.numel(), _stream_ptr(stream)))
     return out
+
+
+class _On:
+    """The device of a call's tensors made current, and the call's stream: the
+    given one, else the device's current one.  What is allocated inside belongs
+    to that stream, so scratch memory that is freed when the call returns is
+    not handed out again before the call's kernels are done with it."""
+
+    __slots__ = ("dev", "stream", "prev")
+
+    def __init__(self, dev: torch.device, stream=None):
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, got {dev}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        self.prev = None
+        if self.stream is not None:
+            self.prev = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.dev.index:
+            self.prev = torch.cuda.device(self.dev)
+        if self.prev is not None:
+            self.prev.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            self.prev.__exit__(*exc)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 device tensor")
+    return workspace
+
+
+def domino_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                         stream=None):
+    """x [..., cols] (float32 or bfloat16) in 8 bits with one scale a row; returns
+    (q int8 like x, scale float32 [...]).  An LM head gets a scale per channel,
+    hidden states one per token."""
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., cols]")
+    _need(x, "x", x.dtype, x.shape, x.device)
+    cols, rows = x.shape[-1], x.shape[:-1].numel()
+    with _On(x.device, stream) as st:
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _need(q, "q", torch.int8, x.shape, x.device)
+        _need(scale, "scale", torch.float32, x.shape[:-1], x.device)
+        _check("domino_quantize_rows", load_library().domino_quantize_rows(
+            rows, cols, DOMINO_BF16 if x.dtype == torch.bfloat16 else DOMINO_F32, _ptr(x), _ptr(q), _ptr(scale), st))
+    return q, scale
+
+
+def domino_base_logits_i8(hidden_q: torch.Tensor, hidden_scale: torch.Tensor, lm_head_q: torch.Tensor,
+                          lm_head_scale: torch.Tensor, base_logits: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Base logits [batch, block, vocab] from hidden states [batch, block, d] and an LM
+    head [vocab, d] in 8 bits (domino_quantize_rows)."""
+    if hidden_q.dim() != 3 or lm_head_q.dim() != 2:
+        raise ValueError("hidden_q must be [batch, block, d] and lm_head_q [vocab, d]")
+    B, K, d = hidden_q.shape
+    V, dev = lm_head_q.shape[0], lm_head_q.device
+    _need(hidden_q, "hidden_q", torch.int8, (B, K, d), dev)
+    _need(hidden_scale, "hidden_scale", torch.float32, (B, K), dev)
+    _need(lm_head_q, "lm_head_q", torch.int8, (V, d), dev)
+    _need(lm_head_scale, "lm_head_scale", torch.float32, (V,), dev)
+    with _On(dev, stream) as st:
+        if base_logits is None:
+            base_logits = torch.empty((B, K, V), dtype=torch.float32, device=dev)
+        _need(base_logits, "base_logits", torch.float32, (B, K, V), dev)
+        _check("domino_base_logits_i8", load_library().domino_base_logits_i8(
+            B, K, d, V, _ptr(hidden_q), _ptr(hidden_scale), _ptr(lm_head_q), _ptr(lm_head_scale), _ptr(base_logits),
+            st))
+    return base_logits
+
+
+def domino_token_logprobs_workspace_size(batch: int, block: int, vocab: int) -> int:
+    return int(load_library().domino_token_logprobs_workspace_size(int(batch), int(block), int(vocab)))
+
+
+def domino_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0,
+                          weights: Optional[torch.Tensor] = None, logp: Optional[torch.Tensor] = None,
+                          entropy: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """log softmax(logits / T) at each position's token, [batch, block]; the entropy of
+    each position is written when a tensor is given.  Positions of weight 0 are not read."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [batch, block, vocab]")
+    B, K, V = logits.shape
+    dev = logits.device
+    _need(logits, "logits", torch.float32, (B, K, V), dev)
+    _need(tokens, "tokens", torch.int32, (B, K), dev)
+    for t, name in ((weights, "weights"), (entropy, "entropy")):
+        if t is not None:
+            _need(t, name, torch.float32, (B, K), dev)
+    with _On(dev, stream) as st:
+        if logp is None:
+            logp = torch.empty((B, K), dtype=torch.float32, device=dev)
+        _need(logp, "logp", torch.float32, (B, K), dev)
+        if workspace is None:
+            workspace = _workspace(None, domino_token_logprobs_workspace_size(B, K, V), dev)
+        ws = _workspace(workspace, 0, dev)
+        _check("domino_token_logprobs", load_library().domino_token_logprobs(
+            B, K, V, _ptr(logits), _ptr(tokens), _ptr(weights), float(temperature), _ptr(logp), _ptr(entropy),
+            _ptr(ws), ws.numel(), st))
+    return logp
+
+
+def domino_policy_loss_workspace_size(batch: int, block: int, vocab: int) -> int:
+    return int(load_library().domino_policy_loss_workspace_size(int(batch), int(block), int(vocab)))
+
+
+def domino_policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                       clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                       ref_logp: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                       temperature: float = 1.0, loss: Optional[torch.Tensor] = None,
+                       logp: Optional[torch.Tensor] = None, kl: Optional[torch.Tensor] = None,
+                       grad: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """The clipped policy loss with its divergence penalty (a one-element device tensor); the
+    positions' log-probabilities and divergences and the gradient of the logits are
+    written when given (grad may be the logits themselves).  The weights carry the mask
+    and the normalisation; None is 1 / (batch * block) everywhere."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [batch, block, vocab]")
+    B, K, V = logits.shape
+    dev = logits.device
+    _need(logits, "logits", torch.float32, (B, K, V), dev)
+    _need(tokens, "tokens", torch.int32, (B, K), dev)
+    _need(old_logp, "old_logp", torch.float32, (B, K), dev)
+    _need(advantages, "advantages", torch.float32, (B, K), dev)
+    for t, name in ((ref_logp, "ref_logp"), (weights, "weights"), (logp, "logp"), (kl, "kl")):
+        if t is not None:
+            _need(t, name, torch.float32, (B, K), dev)
+    if grad is not None:
+        _need(grad, "grad", torch.float32, (B, K, V), dev)
+    with _On(dev, stream) as st:
+        if loss is None:
+            loss = torch.zeros((1,), dtype=torch.float32, device=dev)
+        _need(loss, "loss", torch.float32, (1,), dev)
+        if workspace is None:
+            workspace = _workspace(None, domino_policy_loss_workspace_size(B, K, V), dev)
+        ws = _workspace(workspace, 0, dev)
+        _check("domino_policy_loss", load_library().domino_policy_loss(
+            B, K, V, _ptr(logits), _ptr(tokens), _ptr(old_logp), _ptr(ref_logp), _ptr(advantages), _ptr(weights),
+            float(temperature), float(clip_low), float(clip_high), float(kl_coef), _ptr(loss), _ptr(logp), _ptr(kl),
+            _ptr(grad), _ptr(ws), ws.numel(), st))
+    return loss
 
 
 def domino_debug_read_stream(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdomino.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 SOURCES = ["kernels.hip", "rowstream.hip", "gemm.hip", "loop.hip", "loop_b1.hip", "loop_bn.hip", "verify.hip", "base_draft.hip",
-           "loss.hip", "backward.hip", "gru_backward.hip", "noalloc.hip", "api.cpp", "validate.cpp"]
+           "loss.hip", "backward.hip", "gru_backward.hip", "quantize.hip", "gemm_i8.hip", "policy.hip", "noalloc.hip", "api.cpp", "validate.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

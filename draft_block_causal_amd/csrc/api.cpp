@@ -316,6 +316,64 @@ extern "C" int domino_base_draft(int32_t batch, int32_t block, int32_t vocab, co
                                               workspace, static_cast<hipStream_t>(stream)));
 }
 
+extern "C" int domino_quantize_rows(int32_t rows, int32_t cols, int32_t dtype, const void* x, int8_t* q, float* scale,
+                                    void* stream) {
+  int st = domino::check_quantize_args(rows, cols, dtype, x, q, scale);
+  if (st != DOMINO_OK || rows == 0) return st;
+  return hip_status(domino::launch_quantize_rows(rows, cols, dtype, x, q, scale, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab, const int8_t* hidden_q,
+                                     const float* hidden_scale, const int8_t* lm_head_q, const float* lm_head_scale,
+                                     float* base_logits, void* stream) {
+  int st = domino::check_base_i8_args(batch, block, d, vocab, hidden_q, hidden_scale, lm_head_q, lm_head_scale,
+                                      base_logits);
+  if (st != DOMINO_OK || batch == 0) return st;
+  const int num_cu = device_cu_count();
+  if (num_cu <= 0) return DOMINO_ERR_HIP;
+  return hip_status(domino::launch_gemm_i8(hidden_q, hidden_scale, batch * block, lm_head_q, lm_head_scale, vocab, d,
+                                           base_logits, num_cu, static_cast<hipStream_t>(stream)));
+}
+
+static size_t policy_workspace_size(int32_t batch, int32_t block, int32_t vocab) {
+  if (batch < 1 || batch > domino::kMaxPolicyBatch || block < 1 || block > domino::kMaxPolicyBlock || vocab < 1 ||
+      vocab > domino::kMaxVocab || (long)batch * block > domino::kMaxPolicyRows)
+    return 0;
+  return domino::policy_plan(batch, block, vocab).total;
+}
+
+extern "C" size_t domino_token_logprobs_workspace_size(int32_t batch, int32_t block, int32_t vocab) {
+  return policy_workspace_size(batch, block, vocab);
+}
+
+extern "C" size_t domino_policy_loss_workspace_size(int32_t batch, int32_t block, int32_t vocab) {
+  return policy_workspace_size(batch, block, vocab);
+}
+
+extern "C" int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float* logits,
+                                     const int32_t* tokens, const float* weights, float temperature, float* logp,
+                                     float* entropy, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = domino::check_logprobs_args(batch, block, vocab, logits, tokens, weights, temperature, logp, entropy,
+                                       workspace, workspace_bytes);
+  if (st != DOMINO_OK || batch == 0) return st;
+  return hip_status(domino::launch_token_logprobs(batch, block, vocab, logits, tokens, weights, temperature, logp,
+                                                  entropy, domino::policy_plan(batch, block, vocab), workspace,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+extern "C" int domino_policy_loss(int32_t batch, int32_t block, int32_t vocab, const float* logits,
+                                  const int32_t* tokens, const float* old_logp, const float* ref_logp,
+                                  const float* advantages, const float* weights, float temperature, float clip_low,
+                                  float clip_high, float kl_coef, float* loss, float* logp, float* kl, float* grad,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  const domino::PolicyArgs a{batch,    block,       vocab,    logits,    tokens,  old_logp, ref_logp, advantages, weights,
+                             temperature, clip_low, clip_high, kl_coef, loss,     logp,     kl,       grad};
+  int st = domino::check_policy_args(a, workspace, workspace_bytes);
+  if (st != DOMINO_OK || batch == 0) return st;
+  return hip_status(domino::launch_policy_loss(a, domino::policy_plan(batch, block, vocab), workspace,
+                                               static_cast<hipStream_t>(stream)));
+}
+
 extern "C" int domino_debug_read_stream(const void* buf, size_t bytes, uint32_t* sink, void* stream) {
   if (!sink || (bytes > 0 && !buf)) return DOMINO_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(buf) & 15u) || (reinterpret_cast<uintptr_t>(sink) & 3u)) return DOMINO_ERR_ALIGN;

@@ -224,6 +224,119 @@ int check_verify_args(int32_t batch, int32_t block, int32_t vocab, const float* 
   return DOMINO_OK;
 }
 
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte (a null
+// pointer is no range).
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || !na || !nb) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < na : x - y < nb;
+}
+
+int check_quantize_args(int32_t rows, int32_t cols, int32_t dtype, const void* x, const int8_t* q,
+                        const float* scale) {
+  if (dtype != DOMINO_F32 && dtype != DOMINO_BF16) return DOMINO_ERR_DTYPE;
+  if (rows < 0 || rows > kMaxVocab || cols < 32 || cols > kMaxI8Cols || cols % 32) return DOMINO_ERR_SHAPE;
+  if (rows == 0) return DOMINO_OK;
+  if (!x || !q || !scale) return DOMINO_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || (reinterpret_cast<uintptr_t>(scale) & 3u)) return DOMINO_ERR_ALIGN;
+  const size_t n = (size_t)rows * cols, nx = n * elem_size(dtype), ns = (size_t)rows * 4;
+  if (overlap(x, nx, q, n) || overlap(x, nx, scale, ns) || overlap(q, n, scale, ns)) return DOMINO_ERR_ARG;
+  return DOMINO_OK;
+}
+
+int check_base_i8_args(int32_t batch, int32_t block, int32_t d, int32_t vocab, const int8_t* hidden_q,
+                       const float* hidden_scale, const int8_t* lm_head_q, const float* lm_head_scale,
+                       const float* base_logits) {
+  if (batch < 0 || block < 1 || block > kMaxBlock || d < 32 || d > kMaxI8Cols || d % 32 || vocab < 1 ||
+      vocab > kMaxVocab)
+    return DOMINO_ERR_SHAPE;
+  if (batch > kMaxBatch) return DOMINO_ERR_UNSUPPORTED;
+  if (batch == 0) return DOMINO_OK;
+  if (!hidden_q || !hidden_scale || !lm_head_q || !lm_head_scale || !base_logits) return DOMINO_ERR_NULL;
+  if (!aligned16(hidden_q) || !aligned16(lm_head_q) || !aligned16(base_logits) ||
+      (reinterpret_cast<uintptr_t>(hidden_scale) & 3u) || (reinterpret_cast<uintptr_t>(lm_head_scale) & 3u))
+    return DOMINO_ERR_ALIGN;
+  const size_t M = (size_t)batch * block, N = (size_t)vocab, D = (size_t)d;
+  if (overlap(base_logits, M * N * 4, hidden_q, M * D) || overlap(base_logits, M * N * 4, hidden_scale, M * 4) ||
+      overlap(base_logits, M * N * 4, lm_head_q, N * D) || overlap(base_logits, M * N * 4, lm_head_scale, N * 4))
+    return DOMINO_ERR_ARG;
+  return DOMINO_OK;
+}
+
+static bool bad_temperature(float t) {
+  return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(1.4426950408889634f / t);
+}
+
+static bool policy_shape(int32_t batch, int32_t block, int32_t vocab) {
+  return batch >= 0 && batch <= kMaxPolicyBatch && block >= 1 && block <= kMaxPolicyBlock && vocab >= 1 &&
+         vocab <= kMaxVocab;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// Whether an output overlaps an input or an output before it.
+static bool any_overlap(std::initializer_list<Range> in, std::initializer_list<Range> out) {
+  for (const Range* o = out.begin(); o != out.end(); ++o) {
+    for (const Range& i : in)
+      if (overlap(o->p, o->n, i.p, i.n)) return true;
+    for (const Range* q = out.begin(); q != o; ++q)
+      if (overlap(o->p, o->n, q->p, q->n)) return true;
+  }
+  return false;
+}
+
+static int check_policy_workspace(int32_t batch, int32_t block, int32_t vocab, const void* workspace, size_t bytes) {
+  return !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                 bytes < policy_plan(batch, block, vocab).total
+             ? DOMINO_ERR_WORKSPACE
+             : DOMINO_OK;
+}
+
+int check_logprobs_args(int32_t batch, int32_t block, int32_t vocab, const float* logits, const int32_t* tokens,
+                        const float* weights, float temperature, const float* logp, const float* entropy,
+                        const void* workspace, size_t workspace_bytes) {
+  if (!policy_shape(batch, block, vocab)) return DOMINO_ERR_SHAPE;
+  if ((long)batch * block > kMaxPolicyRows) return DOMINO_ERR_UNSUPPORTED;
+  if (bad_temperature(temperature)) return DOMINO_ERR_ARG;
+  if (batch == 0) return DOMINO_OK;
+  if (!logits || !tokens || !logp) return DOMINO_ERR_NULL;
+  for (const void* q : {(const void*)logits, (const void*)tokens, (const void*)weights, (const void*)logp,
+                        (const void*)entropy})
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return DOMINO_ERR_ALIGN;
+  const size_t r = (size_t)batch * block * 4;
+  if (any_overlap({{logits, r * vocab}, {tokens, r}, {weights, r}, {workspace, workspace_bytes}},
+                  {{logp, r}, {entropy, r}}))
+    return DOMINO_ERR_ARG;
+  return check_policy_workspace(batch, block, vocab, workspace, workspace_bytes);
+}
+
+int check_policy_args(const PolicyArgs& a, const void* workspace, size_t workspace_bytes) {
+  if (!policy_shape(a.B, a.K, a.V)) return DOMINO_ERR_SHAPE;
+  if ((long)a.B * a.K > kMaxPolicyRows) return DOMINO_ERR_UNSUPPORTED;
+  if (bad_temperature(a.temperature)) return DOMINO_ERR_ARG;
+  if (!std::isfinite(a.clip_low) || a.clip_low < 0.f || a.clip_low > 1.f) return DOMINO_ERR_ARG;
+  if (!std::isfinite(a.clip_high) || a.clip_high < 0.f) return DOMINO_ERR_ARG;
+  if (!std::isfinite(a.kl_coef) || a.kl_coef < 0.f) return DOMINO_ERR_ARG;
+  if (a.B == 0) return DOMINO_OK;
+  if (!a.logits || !a.tokens || !a.old_logp || !a.advantages || !a.loss) return DOMINO_ERR_NULL;
+  if (!a.ref_logp && a.kl_coef != 0.f) return DOMINO_ERR_NULL;
+  for (const void* q : {(const void*)a.logits, (const void*)a.tokens, (const void*)a.old_logp,
+                        (const void*)a.ref_logp, (const void*)a.advantages, (const void*)a.weights,
+                        (const void*)a.loss, (const void*)a.logp, (const void*)a.kl, (const void*)a.grad})
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return DOMINO_ERR_ALIGN;
+  const size_t r = (size_t)a.B * a.K * 4, n = r * a.V;
+  // (a gradient in the logits' own buffer is the one overlap allowed)
+  const bool in_place = a.grad == a.logits;
+  if (any_overlap({{in_place ? nullptr : a.logits, n}, {a.tokens, r}, {a.old_logp, r}, {a.ref_logp, r},
+                   {a.advantages, r}, {a.weights, r}, {workspace, workspace_bytes}},
+                  {{a.grad, n}, {a.loss, 4}, {a.logp, r}, {a.kl, r}}))
+    return DOMINO_ERR_ARG;
+  return check_policy_workspace(a.B, a.K, a.V, workspace, workspace_bytes);
+}
+
 }  // namespace domino
 
 extern "C" const char* domino_status_string(int status) {

@@ -6,6 +6,7 @@
 
 #include "../../include/domino.h"
 #include "loss_plan.h"
+#include "policy_plan.h"
 #include "verify_plan.h"
 
 namespace domino {
@@ -59,6 +60,16 @@ int check_gru_backward_args(const domino_head* h, int32_t batch, const int32_t* 
 int check_verify_args(int32_t batch, int32_t block, int32_t vocab, const float* target_logits,
                       const float* draft_logits, const int32_t* draft, float temperature, const int32_t* accept,
                       const int32_t* next_token, const void* workspace, size_t workspace_bytes);
+
+constexpr int kMaxI8Cols = 8192;  // an int32 sum of 8192 products of two 8-bit values stays below 2^27 + 1
+int check_quantize_args(int32_t rows, int32_t cols, int32_t dtype, const void* x, const int8_t* q, const float* scale);
+int check_base_i8_args(int32_t batch, int32_t block, int32_t d, int32_t vocab, const int8_t* hidden_q,
+                       const float* hidden_scale, const int8_t* lm_head_q, const float* lm_head_scale,
+                       const float* base_logits);
+int check_logprobs_args(int32_t batch, int32_t block, int32_t vocab, const float* logits, const int32_t* tokens,
+                        const float* weights, float temperature, const float* logp, const float* entropy,
+                        const void* workspace, size_t workspace_bytes);
+int check_policy_args(const PolicyArgs& a, const void* workspace, size_t workspace_bytes);
 
 // Enqueues a draft call whose arguments passed check_draft_io, over a
 // workspace of at least workspace_layout(h, batch).total bytes, 256-byte

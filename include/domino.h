@@ -387,6 +387,129 @@ int domino_gru_backward(const domino_head *head, int32_t batch, const int32_t *x
 int domino_gru_backward_workspace_size(const domino_head *head, int32_t batch, size_t *bytes);
 
 /*
+ * Rows of float values in 8 bits, symmetric with one scale a row: the form in
+ * which domino_base_logits_i8 takes the frozen LM head (a scale per channel)
+ * and the hidden states (a scale per token).  With a = max_k |x[r, k]|:
+ *   scale[r] = a / 127,   q[r, k] = x[r, k] * 127 / a rounded to the nearest
+ *   integer, ties to even (the exact quotient is rounded, not a rounded one)
+ * so q lies in -127 ... 127 and x is about q * scale, off by at most scale / 2.
+ * A row of zeros has scale 0 and q 0.  A row that holds an infinity or NaN has
+ * scale NaN and q 0: what is computed from it is NaN, and no other row's is.
+ *
+ * x [rows, cols] dtype (domino_dtype), 16-byte aligned; q [rows, cols] int8
+ * (output), 16-byte aligned; scale [rows] float32 (output), 4-byte aligned.
+ * q and scale overlap neither x nor each other (else DOMINO_ERR_ARG).
+ * rows in 0 ... 2^24 - 1 (0 is a no-op); cols a multiple of 32, 32 ... 8192.
+ */
+int domino_quantize_rows(int32_t rows, int32_t cols, int32_t dtype, const void *x, int8_t *q, float *scale,
+                         void *stream);
+
+/*
+ * Base logits from an LM head in 8 bits (domino_quantize_rows), for callers
+ * that trade the last digits of the logits for half the bytes of the LM head:
+ *   base_logits[b, i, v] = hidden_scale[b, i] lm_head_scale[v]
+ *                          sum_k hidden_q[b, i, k] lm_head_q[v, k]
+ * The sums are exact (int32); each is converted to float32 once and multiplied
+ * by the row's scale, then by the channel's.  The result has the layout of
+ * domino_base_logits and is passed on to domino_draft_block or
+ * domino_base_draft.
+ *
+ * hidden_q [batch, block, d] and lm_head_q [vocab, d] int8, 16-byte aligned;
+ * hidden_scale [batch, block], lm_head_scale [vocab] float32, 4-byte aligned;
+ * base_logits [batch, block, vocab] float32 (output), 16-byte aligned; it
+ * overlaps no input (else DOMINO_ERR_ARG).
+ * batch in 0 ... 128 (0 is a no-op; more: DOMINO_ERR_UNSUPPORTED), block in
+ * 1 ... 64, d a multiple of 32, 32 ... 8192, vocab in 1 ... 2^24 - 1.
+ */
+int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab, const int8_t *hidden_q,
+                          const float *hidden_scale, const int8_t *lm_head_q, const float *lm_head_scale,
+                          float *base_logits, void *stream);
+
+/*
+ * Log-probabilities of drafted tokens, and the entropy of the distributions
+ * they were drafted from: with z = logits[b, i] / T and y = tokens[b, i],
+ *   logp[b, i]    = z_y - log sum_v exp z_v
+ *   entropy[b, i] = -sum_v p_v log p_v,  p = softmax(z)     (NULL: skipped)
+ * A position whose weight is 0 (a draft cut short, a padded batch) is not
+ * read: its outputs are 0 and its logits may hold anything.  Logits may be
+ * -inf (entries of probability 0); a row of which every entry is -inf has no
+ * distribution: its logp is -inf and its entropy 0.  A row that holds NaN or
+ * +inf gives NaN outputs of its own and leaves the others alone.
+ *
+ * logits      [batch, block, vocab] float32 (4-byte aligned)
+ * tokens      [batch, block] int32; ids outside [0, vocab) are clamped
+ * weights     [batch, block] float32, or NULL: every position counts
+ * temperature T > 0 with T and log2(e) / T finite (else DOMINO_ERR_ARG)
+ * logp, entropy [batch, block] float32 (outputs); they overlap no input and
+ *             not each other (else DOMINO_ERR_ARG)
+ * workspace   device scratch of at least domino_token_logprobs_workspace_size()
+ *             bytes, 256-byte aligned; its contents are overwritten.
+ * batch in 0 ... 2^20 (0 is a no-op), block in 1 ... 1024, vocab in 1 ...
+ * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).  Arithmetic: exponentials and their sums in float32, merged over
+ * vocabulary slices in a fixed order (repeated calls give the same bits); the
+ * logarithm and the differences in float64.
+ */
+int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
+                          const float *weights, float temperature, float *logp, float *entropy, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Workspace bytes domino_token_logprobs needs (0 for sizes out of range). */
+size_t domino_token_logprobs_workspace_size(int32_t batch, int32_t block, int32_t vocab);
+
+/*
+ * Clipped policy loss of drafted tokens with a penalty on the divergence from
+ * a reference (Schulman et al. 2017, eq. 7, with a separate upper limit), and
+ * its gradient with respect to the logits, for training the draft head on the
+ * acceptance of its own samples.  With logp as domino_token_logprobs gives it
+ * from `logits`, and for each position with weight w != 0:
+ *   ratio = exp(logp - old_logp),  A = advantages
+ *   surrogate = min(ratio A, min(max(ratio, 1 - clip_low), 1 + clip_high) A)
+ *   kl = exp(ref_logp - logp) - (ref_logp - logp) - 1   (>= 0; 0 without ref_logp)
+ *   loss = sum over positions of w (kl_coef kl - surrogate)
+ *   grad[b, i, v] = w (1 / T) g (1[v = y] - p_v),
+ *   g = d(kl_coef kl - surrogate) / d logp
+ *     = kl_coef (1 - exp(ref_logp - logp)) - (ratio A where the surrogate is
+ *       ratio A: ratio <= 1 + clip_high for A >= 0, ratio >= 1 - clip_low for
+ *       A < 0; else 0)
+ * The weights carry both the mask and the normalisation (1 / number of live
+ * positions, say); NULL stands for 1 / (batch * block) everywhere.  The loss
+ * of a call without a live position is 0.
+ * A position whose weight is 0 is not read, nor are its tokens, old_logp,
+ * ref_logp and advantages; its logp, kl and gradient are 0.  A row of which
+ * every logit is -inf has no distribution: logp -inf, kl 0, no loss, gradient
+ * 0.  A live position whose token has probability 0 has an infinite kl where
+ * ref_logp is given; with kl_coef != 0 its gradient is not finite.
+ *
+ * logits      [batch, block, vocab] float32 (4-byte aligned)
+ * tokens      [batch, block] int32; ids outside [0, vocab) are clamped
+ * old_logp    [batch, block] float32, of the policy that drafted the tokens
+ * ref_logp    [batch, block] float32, or NULL (then kl_coef must be 0, else
+ *             DOMINO_ERR_NULL)
+ * advantages  [batch, block] float32;  weights [batch, block] float32 or NULL
+ * temperature as in domino_token_logprobs; clip_low in [0, 1], clip_high >= 0,
+ *             kl_coef >= 0, all finite (else DOMINO_ERR_ARG)
+ * loss        one float32 in device memory (output)
+ * logp, kl    [batch, block] float32 (outputs; NULL: skipped)
+ * grad        [batch, block, vocab] float32 (output; NULL: skipped).  It may
+ *             be the logits' own buffer; otherwise no output overlaps an input
+ *             or another output (else DOMINO_ERR_ARG).
+ * workspace   device scratch of at least domino_policy_loss_workspace_size()
+ *             bytes, 256-byte aligned; its contents are overwritten.
+ * batch in 0 ... 2^20 (0 is a no-op that leaves loss untouched), block in
+ * 1 ... 1024, vocab in 1 ... 2^24 - 1; batch * block <= 2^22 (else
+ * DOMINO_ERR_UNSUPPORTED).  Arithmetic: as domino_token_logprobs;
+ * ratios, divergences and the loss in float64, the loss summed in a fixed
+ * order, so repeated calls give the same bits.
+ */
+int domino_policy_loss(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
+                       const float *old_logp, const float *ref_logp, const float *advantages, const float *weights,
+                       float temperature, float clip_low, float clip_high, float kl_coef, float *loss, float *logp,
+                       float *kl, float *grad, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes domino_policy_loss needs (0 for sizes out of range). */
+size_t domino_policy_loss_workspace_size(int32_t batch, int32_t block, int32_t vocab);
+
+/*
  * Calibration hook: reads `bytes` bytes at `buf` (device memory) once, the way
  * the LM-head streams read (16-byte non-temporal loads, several in flight per
  * thread, a contiguous range for each of 2048 workgroups), and stores into

@@ -5,3 +5,4 @@ Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 """
 from .domino_oracle import *  # noqa: F401,F403
 from .domino_oracle import __all__  # noqa: F401
+from .rollout_oracle import base_logits_i8, policy_loss, quantize_row, quantize_rows, token_logprobs  # noqa: F401
