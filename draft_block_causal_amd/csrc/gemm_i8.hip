@@ -13,6 +13,7 @@
 // first operand, so an accumulator lane holds 4 consecutive columns n of one
 // row m of C, stored as 16 bytes.
 #include <algorithm>
+#include <atomic>
 
 #include "common.h"
 #include "kernels.h"
@@ -25,93 +26,140 @@ __device__ __forceinline__ i32x4 mma16_i8(i32x4 acc, u32x4 w, u32x4 a) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, a), acc, 0, 0, 0);
 }
 
+// Allows a kernel its dynamic LDS, once a device (bit d of `done`).
+static hipError_t allow_lds(const void* kern, int lds, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // ---------------------------------------------------------------------------
-// Streaming kernel, at most 64 rows (G groups of 16): bound by the one read of
-// W.  A workgroup of ceil(K / 512) waves takes a contiguous range of 16-row
-// tiles of W; wave w holds its 512-byte K slice of A in registers (32 a group)
-// and streams the same slice of W: 8 loads of 16 bytes a lane and tile, each
-// two rows' runs of 512 contiguous bytes, non-temporal.  A tile goes through a
-// private 8 KB of LDS into the operand layout (16-byte chunks of row r stored
-// at chunk ^ r, so that both the row-wise writes and the column-wise reads
-// touch 16 bank groups), while the next one is in flight in registers.  The
-// waves' partial sums meet in LDS; finished tiles stay there until kHold of
-// them make runs of 512 bytes a row of C.
+// Streaming kernel: bound by the one read of W.  A workgroup of NW waves takes
+// G groups of 16 rows of A and a contiguous range of 16-row tiles of W; wave w
+// holds its slice of A (64 S bytes of K) in registers and streams the same
+// slice of W: S loads of 16 bytes a lane and tile, contiguous runs of 64 S
+// bytes a row.  A tile goes through private LDS into the operand layout while
+// the next one is in flight in registers.  The waves' partial sums meet in LDS
+// (two buffers in turn, so one barrier a tile); finished tiles stay there until
+// kHold of them make runs of up to 512 bytes a row of C: stores of 64 bytes a
+// row mixed into the stream of W cost it more.
+// More than 64 rows: `parts` workgroups with rows of their own take the same
+// range of W.  They get consecutive numbers on one XCD (workgroups go
+// round-robin over 8), so all but the first read of a tile hit that XCD's L2.
 // W is read through a descriptor sized to the tile's rows below N: the rest,
 // and the prefetch past the range, read as zero without touching memory.
 // Bytes past K within a slice belong to the next row and meet zeros of A.
+// The channel's scale is loaded with its tile: loads return in order, and one
+// issued where it is used would wait for the tile in flight.
 // ---------------------------------------------------------------------------
-constexpr int kSlice = 512;
-constexpr int kSliceTile = 16 * kSlice;  // LDS bytes of one wave's tile
-constexpr int kHold = 8;                 // finished 16-column tiles held in LDS
-
-// LDS: the waves' tiles | red[R][nw][16 G][16] int32 | out[16 G][16 kHold] float.
-// R = 2 (tiles take turns, one barrier a tile) up to 8 waves; 16 waves leave
-// room for one (a second barrier a tile).
-template <int G, int MAXW>
-struct StreamLds {
-  static constexpr int kRed = MAXW > 8 ? 1 : 2;
-  __host__ __device__ static constexpr int red_bytes(int nw) { return nw * G * 1024; }
-  __host__ __device__ static constexpr int out_at(int nw) { return nw * kSliceTile + kRed * red_bytes(nw); }
-  __host__ __device__ static constexpr int total(int nw) { return out_at(nw) + G * kHold * 1024; }
-  static_assert(total(MAXW) <= 160 * 1024, "LDS");
+template <int S, int NW, int G>
+struct Stream {
+  static constexpr int kSlice = 64 * S, kChunks = 4 * S;
+  // LDS row of a tile: 16-byte chunk c of row r.  8 lanes read one chunk of 8
+  // rows at a time, which must fall into 8 groups of banks: chunks are swapped
+  // by the row where their number is a power of two, else rows are padded by a
+  // chunk (S = 5: 84 words, and 84 r mod 32 is different for 8 rows).
+  static constexpr bool kSwap = (S & (S - 1)) == 0;
+  static constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static constexpr int kStride = kSlice + (kSwap ? 0 : 16);
+  static constexpr int kTile = 16 * kStride;
+  static constexpr int kRed = NW * G * 1024;  // bytes of one buffer of partial sums
+  static constexpr int kHold = 8;
+  static constexpr int kOut = NW * kTile + 2 * kRed;
+  static constexpr int kLds = kOut + G * kHold * 1024;
+  static constexpr int kThreads = NW * 64;
+  // workgroups a compute unit: LDS, and 16 waves (8 where the operands take
+  // more than 128 registers)
+  static constexpr int kWaves = G * S > 12 ? 8 : 16;
+  static constexpr int kPerCu = 160 * 1024 / kLds < kWaves / NW ? 160 * 1024 / kLds : kWaves / NW;
+  static_assert(kLds <= 160 * 1024 && kPerCu >= 1, "LDS");
+  __device__ static int at(int r, int c) { return r * kStride + ((kSwap ? c ^ (r & kMask) : c) << 4); }
 };
 
-template <int G, int MAXW>
-__global__ void __launch_bounds__(MAXW * 64)
+template <int S, int NW, int G>
+__global__ void __launch_bounds__(NW * 64)
     gemm_i8_stream_kernel(const int8_t* __restrict__ A, const float* __restrict__ as, int M,
                           const int8_t* __restrict__ W, const float* __restrict__ ws, int N, int K,
-                          float* __restrict__ C) {
-  using SL = StreamLds<G, MAXW>;
+                          float* __restrict__ C, int parts, int ranges) {
+  using T = Stream<S, NW, G>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  const int nw = blockDim.x >> 6, wave = wave_id(), lane = threadIdx.x & 63;
-  const int grp = lane >> 4, col = lane & 15;
-  unsigned char* tile = smem + wave * kSliceTile;
-  int* red = reinterpret_cast<int*>(smem + nw * kSliceTile);
-  float* out = reinterpret_cast<float*>(smem + SL::out_at(nw));
+  const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, col = lane & 15;
+  int x = blockIdx.x, y = 0;
+  if (parts > 1) {
+    const int local = x >> 3;
+    y = local % parts;
+    x = (x & 7) + 8 * (local / parts);
+  }
+  const int m0 = y * G * 16;
+  unsigned char* tile = smem + wave * T::kTile;
+  int* red = reinterpret_cast<int*>(smem + NW * T::kTile);
+  float* out = reinterpret_cast<float*>(smem + T::kOut);
 
-  u32x4 af[G][8];
+  u32x4 af[G][S];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int m = g * 16 + col;
+    const int m = m0 + g * 16 + col;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const int k = wave * kSlice + s * 64 + grp * 16;
+    for (int s = 0; s < S; ++s) {
+      const int k = wave * T::kSlice + s * 64 + grp * 16;
       af[g][s] = m < M && k < K ? ld16(A + (size_t)m * K + k) : u32x4{0, 0, 0, 0};
     }
   }
+  // partial sums of the outputs e = threadIdx.x, + kThreads, ...: row e / 16, column e % 16
+  constexpr int kE = (G * 256 + T::kThreads - 1) / T::kThreads;
+  float sm[kE];
+#pragma unroll
+  for (int i = 0; i < kE; ++i) sm[i] = as[min(m0 + (int)(threadIdx.x + i * T::kThreads) / 16, M - 1)];
 
   const long ntiles = (N + 15) >> 4;
-  const int t0 = (int)(ntiles * blockIdx.x / gridDim.x), t1 = (int)(ntiles * (blockIdx.x + 1) / gridDim.x);
-  const int lrow = lane >> 5, lchunk = lane & 31;
-  const int voff = lrow * K + wave * kSlice + lchunk * 16;
-  auto load = [&](int t, u32x4 (&dst)[8]) {
+  const int t0 = (int)(ntiles * x / ranges), t1 = (int)(ntiles * (x + 1) / ranges);
+  int vo[S], lo[S];  // load j: byte offset in the tile's rows of W, and in LDS
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    const int e = j * 64 + lane, r = e / T::kChunks, c = e % T::kChunks;
+    vo[j] = r * K + wave * T::kSlice + c * 16;
+    lo[j] = T::at(r, c);
+  }
+  const int rcol = threadIdx.x & 15;
+  auto load = [&](int t, u32x4 (&dst)[S], float& scale) {
     const int rows = t < t1 ? min(16, N - t * 16) : 0;
+    scale = ws[min(t * 16 + rcol, N - 1)];
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<int8_t*>(W + (rows ? (size_t)t * 16 * K : 0)), (short)0, rows * K, kRsrcWord3);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      dst[j] = __builtin_amdgcn_raw_buffer_load_b128(r, voff + 2 * j * K, 0, kLoadNonTemporal);
+    for (int j = 0; j < S; ++j) dst[j] = __builtin_amdgcn_raw_buffer_load_b128(r, vo[j], 0, kLoadNonTemporal);
   };
   // columns [16 ta, 16 tb) of C from the held tiles
   auto flush = [&](int ta, int tb) {
     const int n0 = ta * 16, cols = min(tb * 16, N) - n0;
-    for (int e = threadIdx.x; e < G * 16 * (kHold * 16); e += blockDim.x) {
-      const int m = e / (kHold * 16), c = e % (kHold * 16);
-      if (m < M && c < cols) C[(size_t)m * N + n0 + c] = out[e];
+    constexpr int kRow = T::kHold * 16;
+    if ((N & 3) == 0) {  // rows of C start at multiples of 16 bytes
+      for (int e = threadIdx.x; e < G * 16 * (kRow / 4); e += T::kThreads) {
+        const int m = e / (kRow / 4), c = e % (kRow / 4) * 4;
+        if (m0 + m < M && c < cols)
+          *reinterpret_cast<f32x4*>(C + (size_t)(m0 + m) * N + n0 + c) = *reinterpret_cast<f32x4*>(out + m * kRow + c);
+      }
+    } else {
+      for (int e = threadIdx.x; e < G * 16 * kRow; e += T::kThreads) {
+        const int m = e / kRow, c = e % kRow;
+        if (m0 + m < M && c < cols) C[(size_t)(m0 + m) * N + n0 + c] = out[e];
+      }
     }
   };
-  auto process = [&](int t, const u32x4 (&w)[8], int* rb) {
+  auto process = [&](int t, const u32x4 (&w)[S], float scale, int* rb) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = 2 * j + lrow;
-      st16(tile + r * kSlice + ((lchunk ^ r) << 4), w[j]);
-    }
+    for (int j = 0; j < S; ++j) st16(tile + lo[j], w[j]);
     i32x4 acc[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[g] = i32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const u32x4 b = ld16(tile + col * kSlice + (((s * 4 + grp) ^ col) << 4));
+    for (int s = 0; s < S; ++s) {
+      const u32x4 b = ld16(tile + T::at(col, s * 4 + grp));
 #pragma unroll
       for (int g = 0; g < G; ++g) acc[g] = mma16_i8(acc[g], b, af[g][s]);
     }
@@ -119,152 +167,181 @@ __global__ void __launch_bounds__(MAXW * 64)
 #pragma unroll
     for (int g = 0; g < G; ++g)
       *reinterpret_cast<i32x4*>(rb + ((wave * G + g) * 16 + col) * 16 + grp * 4) = acc[g];
+    // taken by every wave here: a load that one side of a branch consumes makes
+    // the compiler wait for the tile in flight later
+    asm volatile("" : "+v"(scale));
     __syncthreads();
-    const int held = (t - t0) % kHold;
-    for (int e = threadIdx.x; e < G * 256; e += blockDim.x) {
-      int sum = 0;
-      for (int q = 0; q < nw; ++q) sum += rb[q * G * 256 + e];
-      const int m = e >> 4, n = t * 16 + (e & 15);
-      if (m < M && n < N) out[m * (kHold * 16) + held * 16 + (e & 15)] = (float)sum * as[m] * ws[n];
+    const int held = (t - t0) % T::kHold;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const int e = threadIdx.x + i * T::kThreads;
+      if (kE * T::kThreads == G * 256 || e < G * 256) {
+        int sum = 0;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) sum += rb[q * G * 256 + e];
+        out[(e >> 4) * (T::kHold * 16) + held * 16 + rcol] = (float)sum * sm[i] * scale;
+      }
     }
-    if (held == kHold - 1 || t == t1 - 1) {
+    if (held == T::kHold - 1 || t == t1 - 1) {
       __syncthreads();
       flush(t - held, t + 1);
       // (the next write to `out` follows the next tile's barrier)
-    } else if (SL::kRed == 1) {
-      __syncthreads();  // the sums are read before the next tile's are written
     }
   };
 
-  u32x4 w0[8], w1[8];
+  u32x4 w0[S], w1[S];
+  float s0, s1;
   int t = t0;
-  load(t, w0);
+  load(t, w0, s0);
+  // The scheduling barriers keep each prefetch ahead of the LDS traffic of the
+  // tile in hand.
   while (t < t1) {
-    load(t + 1, w1);
+    load(t + 1, w1, s1);
     __builtin_amdgcn_sched_barrier(0);
-    process(t, w0, red);
+    process(t, w0, s0, red);
     if (++t >= t1) break;
-    load(t + 1, w0);
+    load(t + 1, w0, s0);
     __builtin_amdgcn_sched_barrier(0);
-    process(t, w1, red + (SL::kRed - 1) * nw * G * 256);
+    process(t, w1, s1, red + T::kRed / 4);
     ++t;
   }
 }
 
-template <int G, int MAXW>
-static hipError_t launch_stream(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
-                                float* C, int num_cu, hipStream_t s) {
-  const int nw = (K + kSlice - 1) / kSlice;
-  auto kern = gemm_i8_stream_kernel<G, MAXW>;
-  const int lds = StreamLds<G, MAXW>::total(nw);
-  const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+template <int S, int NW, int G>
+static hipError_t launch_stream_g(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N,
+                                  int K, float* C, int parts, int num_cu, hipStream_t s) {
+  using T = Stream<S, NW, G>;
+  auto kern = gemm_i8_stream_kernel<S, NW, G>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), T::kLds, done);
   if (e != hipSuccess) return e;
-  // about 8 waves a compute unit
-  const int per_cu = std::max(1, 8 / nw);
-  const int grid = std::min((N + 15) / 16, num_cu * per_cu);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3((unsigned)nw * 64), lds, s, A, as, M, W, ws, N, K, C);
+  const int ntiles = (N + 15) / 16;
+  int ranges = std::min(ntiles, num_cu * T::kPerCu / parts);
+  if (parts > 1) ranges = std::max(8, ranges / 8 * 8);  // (a range may be empty)
+  hipLaunchKernelGGL(kern, dim3((unsigned)(ranges * parts)), dim3(T::kThreads), T::kLds, s, A, as, M, W, ws, N, K, C,
+                     parts, ranges);
   return hipGetLastError();
 }
 
+// M <= 64 parts rows
+template <int S, int NW>
+static hipError_t launch_stream(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
+                                float* C, int parts, int num_cu, hipStream_t s) {
+  const int groups = ((M + parts - 1) / parts + 15) / 16;
+  switch (groups) {
+    case 1: return launch_stream_g<S, NW, 1>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
+    case 2: return launch_stream_g<S, NW, 2>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
+    case 3: return launch_stream_g<S, NW, 3>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
+    default: return launch_stream_g<S, NW, 4>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Tiled kernel: BM x BN outputs a workgroup of 8 waves (a 2 x 4 grid), operands
-// from memory straight into LDS through a ring of 64-byte K steps, laid out
-// and refilled as in gemm.hip (chunk c of a 64-byte row r in slot
-// c ^ ((r >> 1) & 3)); two groups of waves, one per SIMD each, alternate
-// between reading fragments and multiplying.
+// Tiled kernel: BM x 256 outputs a tile, 8 waves (a 2 x 4 grid), one workgroup
+// a compute unit that walks its tiles without a break: the loads of the next
+// tile are in flight while the last one's results are stored.
+// Operands go from memory straight into LDS (16 bytes a lane), in steps of 128
+// bytes of K: a load instruction covers whole 128-byte lines of 8 rows.  W and
+// A have rings of WS and 2 steps; W's, which comes from HBM, is the deeper.  The
+// first row of waves loads W and the second A: loads are counted back in the
+// order of their issue, and a wave that loaded both would wait for W's later
+// steps whenever it waits for A's next one.
+// Chunk c of a 128-byte LDS row r sits in slot c ^ (r & 7): a 16-byte read is
+// served 8 lanes at a time, and the 8 lanes of a fragment read (8 rows, one
+// chunk) then touch 8 different groups of banks.
+// The two rows of waves alternate, one phase apart: one reads the fragments of
+// half a step (64 bytes of K) and issues loads while the other multiplies,
+// with a barrier between phases.  Order: the loads into a slot are issued one
+// step after its last reads (by both rows of waves, each of which waits for its
+// reads before the barrier that ends them); a wave waits for its part of step
+// D + 1 at the end of its reading in step D's second half, at least one barrier
+// before the first wave reads it.
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(1))) const void* gptr_t;
 typedef __attribute__((address_space(3))) void* lptr_t;
 
 __device__ const unsigned char kZeros[16] = {};  // what A reads past K
 
-template <int BM, int BN>
+template <int BM, int WS>
 struct TileI8 {
-  static constexpr int kThreads = 512, kRow = 64;
-  static constexpr int kStage = (BM + BN) * kRow;
-  static constexpr int kStages = 160 * 1024 / kStage < 6 ? 160 * 1024 / kStage : 6;
-  static constexpr int kRowsPerIssue = 128;  // 8 waves x 16 rows of 64 bytes
-  static constexpr int kALoads = BM / kRowsPerIssue;
-  static constexpr int kWLoads = (BN + kRowsPerIssue - 1) / kRowsPerIssue;
-  static constexpr int kPerStage = kALoads + kWLoads;
-  static constexpr int kFA = BM / 2 / 16, kFW = BN / 4 / 16;
-  static_assert(BM % 128 == 0 && BN % 128 == 0, "whole DMA rounds");
-  static_assert((kStages - 2) * kPerStage < 64, "vector-memory count field");
+  static constexpr int kThreads = 512, kBN = 256, kRow = 128;
+  static constexpr int kABytes = BM * kRow, kWBytes = kBN * kRow;
+  static constexpr int kLds = WS * kWBytes + 2 * kABytes;
+  static constexpr int kAL = BM / 32, kWL = kBN / 32;  // loads of a step per loading wave
+  static constexpr int kFA = BM / 2 / 16, kFW = kBN / 4 / 16;
+  static_assert(BM % 128 == 0 && WS >= 3 && (WS - 2) * kWL < 64, "rings");
+  static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 // vmcnt(n), lgkmcnt(0); expcnt at its maximum
 #define DOMINO_I8_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | 0x0070)
 
-// Until at most `ahead` younger stages of this wave's loads are in flight and
-// its LDS reads have returned.
-template <int PER, int MAXA>
-__device__ __forceinline__ void wait_ahead(int ahead) {
-  if constexpr (MAXA >= 4) {
-    if (ahead >= 4) {
-      DOMINO_I8_WAIT(4 * PER);
-      return;
-    }
-  }
-  if constexpr (MAXA >= 3) {
-    if (ahead >= 3) {
-      DOMINO_I8_WAIT(3 * PER);
-      return;
-    }
-  }
-  if (ahead >= 2) {
-    DOMINO_I8_WAIT(2 * PER);
-  } else if (ahead == 1) {
-    DOMINO_I8_WAIT(PER);
-  } else {
-    DOMINO_I8_WAIT(0);
-  }
-}
-
-template <int BM, int BN>
+template <int BM, int WS>
 __global__ void __launch_bounds__(512, 1)
     gemm_i8_tiled_kernel(const int8_t* __restrict__ A, const float* __restrict__ as, int M,
                          const int8_t* __restrict__ W, const float* __restrict__ ws, int N, int K,
                          float* __restrict__ C, int num_m, int num_n) {
-  using T = TileI8<BM, BN>;
+  using T = TileI8<BM, WS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  // one XCD takes every M tile of an N tile back to back (workgroups go
-  // round-robin over 8 XCDs): W comes from memory once and from its L2 after
-  const int xcd = blockIdx.x % 8, local = blockIdx.x / 8;
-  const int nl = local / num_m, mt = local - nl * num_m, nt = nl * 8 + xcd;
-  if (nt >= num_n) return;
-  const int m0 = mt * BM, n0 = nt * BN;
   const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, col = lane & 15;
   const int wm = wave >> 2, wn = wave & 3;
+  // one XCD takes every M tile of an N tile back to back (workgroups go
+  // round-robin over 8 XCDs): W comes from memory once and from its L2 after
+  const int xcd = blockIdx.x & 7, per_xcd = gridDim.x >> 3;
+  const int xcd_tiles = ((num_n + 7 - xcd) >> 3) * num_m;  // N tiles xcd, xcd + 8, ...
+  const int first = blockIdx.x >> 3;
+  if (first >= xcd_tiles) return;
+  const int mine = (xcd_tiles - first + per_xcd - 1) / per_xcd;
+  const int nd = (K + 127) >> 7;
+  const int total = mine * nd;  // steps of all tiles
+  auto tile_at = [&](int i, int& m0, int& n0) {
+    const int l = first + i * per_xcd, nl = l / num_m;
+    m0 = (l - nl * num_m) * BM;
+    n0 = (nl * 8 + xcd) * T::kBN;
+  };
 
-  const int dchunk = (lane & 3) ^ ((lane >> 3) & 3);
-  const int8_t *ag[T::kALoads], *wg[T::kWLoads];
+  // loading: load i of wave w covers rows 32 i + 8 (w & 3) .. + 7 of the operand
+  const bool loads_w = wm == 0;
+  const int lrow = (wave & 3) * 8 + (lane >> 3), chunk = (lane & 7) ^ (lane >> 3);
+  // this lane's bytes of a tile's last step lie past K: A reads zeros there, W
+  // its row's first bytes of the step
+  const bool past = (nd - 1) * 128 + chunk * 16 >= K;
+  const int8_t* base = A;  // the tile's first row
+  int last_row = 0;        // the operand's last row, counted from it
+  int it = 0, id = 0, islot = 0;  // the next step to load: tile, step, ring slot
+  auto seek = [&]() {
+    int m0, n0;
+    tile_at(it, m0, n0);
+    const int r0 = loads_w ? n0 : m0, rows = loads_w ? N : M;
+    base = (loads_w ? W : A) + (size_t)r0 * K;
+    last_row = rows - 1 - r0;
+  };
+  auto issue = [&]() {
+    const bool skip = past && id == nd - 1;
+    const int8_t* p = base + id * 128;
+    const uint32_t c16 = chunk * 16;
+    if (loads_w) {
+      unsigned char* dst = smem + islot * T::kWBytes + (wave & 3) * 1024;
 #pragma unroll
-  for (int i = 0; i < T::kALoads; ++i)
-    ag[i] = A + (size_t)min(m0 + i * 128 + wave * 16 + (lane >> 2), M - 1) * K + dchunk * 16;
+      for (int i = 0; i < T::kWL; ++i)
+        __builtin_amdgcn_global_load_lds((gptr_t)(p + (uint32_t)(min(i * 32 + lrow, last_row) * K) + (skip ? 0 : c16)),
+                                         (lptr_t)(dst + i * 4096), 16, 0, 0);
+      if (++islot == WS) islot = 0;
+    } else {
+      unsigned char* dst = smem + WS * T::kWBytes + islot * T::kABytes + (wave & 3) * 1024;
 #pragma unroll
-  for (int i = 0; i < T::kWLoads; ++i)
-    wg[i] = W + (size_t)min(n0 + i * 128 + wave * 16 + (lane >> 2), N - 1) * K + dchunk * 16;
-  const int nk = (K + 63) / 64;
-  const bool past = K % 64 != 0 && dchunk >= 2;  // this lane's chunk of the last step lies past K
-  auto issue = [&](int kt) {
-    unsigned char* sA = smem + (kt % T::kStages) * T::kStage;
-    unsigned char* sW = sA + BM * T::kRow;
-    const bool skip = past && kt == nk - 1;
-    const size_t k = (size_t)kt * 64;
-#pragma unroll
-    for (int i = 0; i < T::kALoads; ++i) {
-      const void* p = ag[i] + k;
-      if (skip) p = kZeros;
-      __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)(sA + (i * 128 + wave * 16) * 64), 16, 0, 0);
+      for (int i = 0; i < T::kAL; ++i) {
+        const void* q = p + (uint32_t)(min(i * 32 + lrow, last_row) * K) + c16;
+        if (skip) q = kZeros;
+        __builtin_amdgcn_global_load_lds((gptr_t)q, (lptr_t)(dst + i * 4096), 16, 0, 0);
+      }
+      islot ^= 1;
     }
-#pragma unroll
-    for (int i = 0; i < T::kWLoads; ++i) {
-      const void* p = wg[i] + (skip ? k - 32 : k);  // (any bytes of the row: they meet zeros)
-      __builtin_amdgcn_global_load_lds((gptr_t)p, (lptr_t)(sW + (i * 128 + wave * 16) * 64), 16, 0, 0);
+    if (++id == nd) {
+      id = 0;
+      if (++it < mine) seek();
     }
   };
-  const int fslot = (grp ^ ((col >> 1) & 3)) * 16;
 
   i32x4 acc[T::kFA][T::kFW];
 #pragma unroll
@@ -272,75 +349,135 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
     for (int j = 0; j < T::kFW; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
+  // The tile's scales: loaded at its start, taken (the empty asm) behind a wait
+  // that the operands need anyway.  Loaded where they are used, every store
+  // would wait for the loads in flight.
+  float sn[T::kFW][4], sm[T::kFA];
+  int m0, n0;
+  auto scales = [&]() {
 #pragma unroll
-  for (int s = 0; s < T::kStages - 1; ++s)
-    if (s < nk) issue(s);
-  wait_ahead<T::kPerStage, T::kStages - 2>(min(T::kStages - 2, nk - 1));
-  __builtin_amdgcn_s_barrier();
-  if (wm == 1) __builtin_amdgcn_s_barrier();  // the second group starts one phase later
-  for (int kt = 0; kt < nk; ++kt) {
-    __builtin_amdgcn_sched_barrier(0);
-    const unsigned char* sA = smem + (kt % T::kStages) * T::kStage;
-    const unsigned char* sW = sA + BM * T::kRow;
-    u32x4 af[T::kFA], wf[T::kFW];
+    for (int j = 0; j < T::kFW; ++j)
 #pragma unroll
-    for (int i = 0; i < T::kFA; ++i) af[i] = ld16(sA + ((wm * T::kFA + i) * 16 + col) * 64 + fslot);
+      for (int q = 0; q < 4; ++q) sn[j][q] = ws[min(n0 + (wn * T::kFW + j) * 16 + grp * 4 + q, N - 1)];
 #pragma unroll
-    for (int j = 0; j < T::kFW; ++j) wf[j] = ld16(sW + ((wn * T::kFW + j) * 16 + col) * 64 + fslot);
-    if (kt + T::kStages - 1 < nk) issue(kt + T::kStages - 1);
-    wait_ahead<T::kPerStage, T::kStages - 2>(max(0, min(T::kStages - 2, nk - 2 - kt)));
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < T::kFA; ++i) sm[i] = as[min(m0 + (wm * T::kFA + i) * 16 + col, M - 1)];
+  };
+  auto take_scales = [&]() {
 #pragma unroll
-    for (int i = 0; i < T::kFA; ++i)
+    for (int j = 0; j < T::kFW; ++j)
 #pragma unroll
-      for (int j = 0; j < T::kFW; ++j) acc[i][j] = mma16_i8(acc[i][j], wf[j], af[i]);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_barrier();
-  }
-  if (wm == 0) __builtin_amdgcn_s_barrier();  // equal barrier counts in both groups
-
+      for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(sn[j][q]));
+#pragma unroll
+    for (int i = 0; i < T::kFA; ++i) asm volatile("" : "+v"(sm[i]));
+  };
   const bool vec = (N & 3) == 0;  // then every group of 4 columns is 16-byte aligned and whole
+  auto store = [&]() {
+    if (vec && m0 + BM <= M && n0 + T::kBN <= N) {  // a whole tile
+      float* c = C + (size_t)(m0 + wm * T::kFA * 16 + col) * N + n0 + wn * T::kFW * 16 + grp * 4;
 #pragma unroll
-  for (int j = 0; j < T::kFW; ++j) {
-    const int n = n0 + (wn * T::kFW + j) * 16 + grp * 4;
-    if (n >= N) continue;
-    float sn[4];
+      for (int i = 0; i < T::kFA; ++i) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sn[q] = ws[min(n + q, N - 1)];
+        for (int j = 0; j < T::kFW; ++j) {
+          f32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sm[i] * sn[j][q];
+          acc[i][j] = i32x4{0, 0, 0, 0};
+          *reinterpret_cast<f32x4*>(c + j * 16) = v;
+        }
+        c += (size_t)16 * N;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < T::kFA; ++i) {
       const int m = m0 + (wm * T::kFA + i) * 16 + col;
-      if (m >= M) continue;
-      const float sm = as[m];
-      float* c = C + (size_t)m * N + n;
-      f32x4 v;
+      float* c = C + (size_t)m * N;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sm * sn[q];
-      if (vec) {
-        *reinterpret_cast<f32x4*>(c) = v;
-      } else {
+      for (int j = 0; j < T::kFW; ++j) {
+        const int n = n0 + (wn * T::kFW + j) * 16 + grp * 4;
+        f32x4 v;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n + q < N) c[q] = v[q];
+        for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sm[i] * sn[j][q];
+        acc[i][j] = i32x4{0, 0, 0, 0};
+        if (m < M) {
+          if (vec) {
+            if (n < N) *reinterpret_cast<f32x4*>(c + n) = v;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (n + q < N) c[n + q] = v[q];
+          }
+        }
       }
     }
+  };
+
+  seek();
+  const int ahead = loads_w ? WS - 1 : 1;
+  for (int q = 0; q < ahead; ++q)
+    if (q < total) issue();
+  DOMINO_I8_WAIT(0);
+  __builtin_amdgcn_s_barrier();
+  if (wm == 1) __builtin_amdgcn_s_barrier();  // the second row of waves starts one phase later
+
+  int d = 0, tile = 0, sa_slot = 0, sw_slot = 0;
+  tile_at(0, m0, n0);
+  for (int g = 0; g < total; ++g) {
+    const unsigned char* sW = smem + sw_slot * T::kWBytes + wn * T::kFW * 2048 + col * 128;
+    const unsigned char* sA = smem + WS * T::kWBytes + sa_slot * T::kABytes + wm * T::kFA * 2048 + col * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int slot = ((h * 4 + grp) ^ (col & 7)) * 16;
+      u32x4 af[T::kFA], wf[T::kFW];
+#pragma unroll
+      for (int j = 0; j < T::kFW; ++j) wf[j] = ld16(sW + j * 2048 + slot);
+#pragma unroll
+      for (int i = 0; i < T::kFA; ++i) af[i] = ld16(sA + i * 2048 + slot);
+      if (h == 0) {
+        if (d == 0) scales();
+        if (g + ahead < total) issue();
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      } else if (loads_w && g + WS - 1 < total) {
+        DOMINO_I8_WAIT((WS - 2) * T::kWL);
+      } else {
+        DOMINO_I8_WAIT(0);
+      }
+      if (h == 1 && d == 0) take_scales();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < T::kFA; ++i)
+#pragma unroll
+        for (int j = 0; j < T::kFW; ++j) acc[i][j] = mma16_i8(acc[i][j], wf[j], af[i]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (h == 1 && d == nd - 1) store();
+      __builtin_amdgcn_s_barrier();
+    }
+    sa_slot ^= 1;
+    if (++sw_slot == WS) sw_slot = 0;
+    if (++d == nd) {
+      d = 0;
+      if (++tile < mine) tile_at(tile, m0, n0);
+    }
   }
+  if (wm == 0) __builtin_amdgcn_s_barrier();  // equal barrier counts in both rows of waves
 }
 
-template <int BM, int BN>
+template <int BM, int WS>
 static hipError_t launch_tiled(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
-                               float* C, hipStream_t s) {
-  using T = TileI8<BM, BN>;
-  const int num_m = (M + BM - 1) / BM, num_n = (N + BN - 1) / BN;
-  const unsigned blocks = (unsigned)((num_n + 7) / 8 * 8) * (unsigned)num_m;
-  auto kern = gemm_i8_tiled_kernel<BM, BN>;
-  const size_t lds = (size_t)T::kStages * T::kStage;
-  const hipError_t e =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                               float* C, int num_cu, hipStream_t s) {
+  using T = TileI8<BM, WS>;
+  const int num_m = (M + BM - 1) / BM, num_n = (N + T::kBN - 1) / T::kBN;
+  // a multiple of 8 workgroups, at most one a compute unit
+  const int want = (num_n + 7) / 8 * num_m, have = std::max(1, num_cu / 8);
+  auto kern = gemm_i8_tiled_kernel<BM, WS>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), T::kLds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(T::kThreads), lds, s, A, as, M, W, ws, N, K, C, num_m, num_n);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * std::min(want, have))), dim3(T::kThreads), T::kLds, s, A, as, M, W, ws, N,
+                     K, C, num_m, num_n);
   return hipGetLastError();
 }
 
@@ -348,16 +485,18 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
                           int K, float* C, int num_cu, hipStream_t s) {
   if (M <= 0 || N <= 0) return hipSuccess;
   if (K <= 0 || K % 32 || K > 8192) return hipErrorNotSupported;
-  if (K <= 4096) {
-    if (M <= 16) return launch_stream<1, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
-    if (M <= 32) return launch_stream<2, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
-    if (M <= 48) return launch_stream<3, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
-    if (M <= 64) return launch_stream<4, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
-  } else if (M <= 16) {
-    return launch_stream<1, 16>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  const int parts = (M + 63) / 64;
+  if (K <= 4096 && parts <= 2) {
+    if (K <= 256) return launch_stream<4, 1>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
+    if (K <= 512) return launch_stream<4, 2>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
+    if (K <= 1024) return launch_stream<4, 4>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
+    if (K <= 2048) return launch_stream<4, 8>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
+    if (K <= 2560) return launch_stream<5, 8>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
+    return launch_stream<8, 8>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
   }
-  return M <= 128 ? launch_tiled<128, 256>(A, a_scale, M, W, w_scale, N, K, C, s)
-                  : launch_tiled<256, 256>(A, a_scale, M, W, w_scale, N, K, C, s);
+  if (M <= 16) return launch_stream_g<16, 8, 1>(A, a_scale, M, W, w_scale, N, K, C, 1, num_cu, s);
+  return M <= 128 ? launch_tiled<128, 4>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
+                  : launch_tiled<256, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
 }
 
 }  // namespace domino
