@@ -45,12 +45,11 @@ static hipError_t allow_lds(const void* kern, int lds, std::atomic<uint64_t>& do
 // slice of W: S loads of 16 bytes a lane and tile, contiguous runs of 64 S
 // bytes a row.  A tile goes through private LDS into the operand layout while
 // the next one is in flight in registers.  The waves' partial sums meet in LDS
-// (two buffers in turn, so one barrier a tile); finished tiles stay there until
-// kHold of them make runs of up to 512 bytes a row of C: stores of 64 bytes a
-// row mixed into the stream of W cost it more.
-// More than 64 rows: `parts` workgroups with rows of their own take the same
-// range of W.  They get consecutive numbers on one XCD (workgroups go
-// round-robin over 8), so all but the first read of a tile hit that XCD's L2.
+// (two buffers in turn, so one barrier a tile); finished tiles stay there as
+// long as they fit, all of a workgroup's where they do, since stores mixed into
+// the stream of W cost it more than the same bytes behind it (one block of a
+// Qwen3-8B head: 102 us with a store every 8 tiles, 95 with all at the end,
+// 93 with none).
 // W is read through a descriptor sized to the tile's rows below N: the rest,
 // and the prefetch past the range, read as zero without touching memory.
 // Bytes past K within a slice belong to the next row and meet zeros of A.
@@ -69,15 +68,16 @@ struct Stream {
   static constexpr int kStride = kSlice + (kSwap ? 0 : 16);
   static constexpr int kTile = 16 * kStride;
   static constexpr int kRed = NW * G * 1024;  // bytes of one buffer of partial sums
-  static constexpr int kHold = 8;
   static constexpr int kOut = NW * kTile + 2 * kRed;
-  static constexpr int kLds = kOut + G * kHold * 1024;
+  static constexpr int kLds = kOut + G * 8 * 1024;  // with 8 finished tiles, the least
   static constexpr int kThreads = NW * 64;
   // workgroups a compute unit: LDS, and 16 waves (8 where the operands take
   // more than 128 registers)
   static constexpr int kWaves = G * S > 12 ? 8 : 16;
+  // (as many finished tiles as fit: hold())
   static constexpr int kPerCu = 160 * 1024 / kLds < kWaves / NW ? 160 * 1024 / kLds : kWaves / NW;
   static_assert(kLds <= 160 * 1024 && kPerCu >= 1, "LDS");
+  static int hold(int tiles) { return std::min(tiles, (160 * 1024 / kPerCu - kOut) / (G * 1024)); }
   __device__ static int at(int r, int c) { return r * kStride + ((kSwap ? c ^ (r & kMask) : c) << 4); }
 };
 
@@ -85,17 +85,10 @@ template <int S, int NW, int G>
 __global__ void __launch_bounds__(NW * 64)
     gemm_i8_stream_kernel(const int8_t* __restrict__ A, const float* __restrict__ as, int M,
                           const int8_t* __restrict__ W, const float* __restrict__ ws, int N, int K,
-                          float* __restrict__ C, int parts, int ranges) {
+                          float* __restrict__ C, int hold) {
   using T = Stream<S, NW, G>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, col = lane & 15;
-  int x = blockIdx.x, y = 0;
-  if (parts > 1) {
-    const int local = x >> 3;
-    y = local % parts;
-    x = (x & 7) + 8 * (local / parts);
-  }
-  const int m0 = y * G * 16;
   unsigned char* tile = smem + wave * T::kTile;
   int* red = reinterpret_cast<int*>(smem + NW * T::kTile);
   float* out = reinterpret_cast<float*>(smem + T::kOut);
@@ -103,7 +96,7 @@ __global__ void __launch_bounds__(NW * 64)
   u32x4 af[G][S];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int m = m0 + g * 16 + col;
+    const int m = g * 16 + col;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const int k = wave * T::kSlice + s * 64 + grp * 16;
@@ -114,10 +107,10 @@ __global__ void __launch_bounds__(NW * 64)
   constexpr int kE = (G * 256 + T::kThreads - 1) / T::kThreads;
   float sm[kE];
 #pragma unroll
-  for (int i = 0; i < kE; ++i) sm[i] = as[min(m0 + (int)(threadIdx.x + i * T::kThreads) / 16, M - 1)];
+  for (int i = 0; i < kE; ++i) sm[i] = as[min((int)(threadIdx.x + i * T::kThreads) / 16, M - 1)];
 
   const long ntiles = (N + 15) >> 4;
-  const int t0 = (int)(ntiles * x / ranges), t1 = (int)(ntiles * (x + 1) / ranges);
+  const int t0 = (int)(ntiles * blockIdx.x / gridDim.x), t1 = (int)(ntiles * (blockIdx.x + 1) / gridDim.x);
   int vo[S], lo[S];  // load j: byte offset in the tile's rows of W, and in LDS
 #pragma unroll
   for (int j = 0; j < S; ++j) {
@@ -137,20 +130,19 @@ __global__ void __launch_bounds__(NW * 64)
   // columns [16 ta, 16 tb) of C from the held tiles
   auto flush = [&](int ta, int tb) {
     const int n0 = ta * 16, cols = min(tb * 16, N) - n0;
-    constexpr int kRow = T::kHold * 16;
-    if ((N & 3) == 0) {  // rows of C start at multiples of 16 bytes
-      for (int e = threadIdx.x; e < G * 16 * (kRow / 4); e += T::kThreads) {
-        const int m = e / (kRow / 4), c = e % (kRow / 4) * 4;
-        if (m0 + m < M && c < cols)
-          *reinterpret_cast<f32x4*>(C + (size_t)(m0 + m) * N + n0 + c) = *reinterpret_cast<f32x4*>(out + m * kRow + c);
-      }
-    } else {
-      for (int e = threadIdx.x; e < G * 16 * kRow; e += T::kThreads) {
-        const int m = e / kRow, c = e % kRow;
-        if (m0 + m < M && c < cols) C[(size_t)(m0 + m) * N + n0 + c] = out[e];
+    const int stride = hold * 16;
+    // a wave takes whole rows; 16 bytes a lane where rows of C start at multiples of 16 bytes
+    for (int m = wave; m < M; m += NW) {
+      float* c = C + (size_t)m * N + n0;
+      const float* o = out + m * stride;
+      if ((N & 3) == 0) {
+        for (int e = lane * 4; e < cols; e += 256) __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(o + e), reinterpret_cast<f32x4*>(c + e));
+      } else {
+        for (int e = lane; e < cols; e += 64) c[e] = o[e];
       }
     }
   };
+  int held = 0;
   auto process = [&](int t, const u32x4 (&w)[S], float scale, int* rb) {
 #pragma unroll
     for (int j = 0; j < S; ++j) st16(tile + lo[j], w[j]);
@@ -171,7 +163,6 @@ __global__ void __launch_bounds__(NW * 64)
     // the compiler wait for the tile in flight later
     asm volatile("" : "+v"(scale));
     __syncthreads();
-    const int held = (t - t0) % T::kHold;
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const int e = threadIdx.x + i * T::kThreads;
@@ -179,13 +170,13 @@ __global__ void __launch_bounds__(NW * 64)
         int sum = 0;
 #pragma unroll
         for (int q = 0; q < NW; ++q) sum += rb[q * G * 256 + e];
-        out[(e >> 4) * (T::kHold * 16) + held * 16 + rcol] = (float)sum * sm[i] * scale;
+        out[(e >> 4) * (hold * 16) + held * 16 + rcol] = (float)sum * sm[i] * scale;
       }
     }
-    if (held == T::kHold - 1 || t == t1 - 1) {
+    if (++held == hold || t == t1 - 1) {
       __syncthreads();
-      flush(t - held, t + 1);
-      // (the next write to `out` follows the next tile's barrier)
+      flush(t + 1 - held, t + 1);  // (the next write to `out` follows the next tile's barrier)
+      held = 0;
     }
   };
 
@@ -209,30 +200,29 @@ __global__ void __launch_bounds__(NW * 64)
 
 template <int S, int NW, int G>
 static hipError_t launch_stream_g(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N,
-                                  int K, float* C, int parts, int num_cu, hipStream_t s) {
+                                  int K, float* C, int num_cu, hipStream_t s) {
   using T = Stream<S, NW, G>;
   auto kern = gemm_i8_stream_kernel<S, NW, G>;
   static std::atomic<uint64_t> done{0};
-  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), T::kLds, done);
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), 160 * 1024, done);
   if (e != hipSuccess) return e;
   const int ntiles = (N + 15) / 16;
-  int ranges = std::min(ntiles, num_cu * T::kPerCu / parts);
-  if (parts > 1) ranges = std::max(8, ranges / 8 * 8);  // (a range may be empty)
-  hipLaunchKernelGGL(kern, dim3((unsigned)(ranges * parts)), dim3(T::kThreads), T::kLds, s, A, as, M, W, ws, N, K, C,
-                     parts, ranges);
+  const int grid = std::min(ntiles, num_cu * T::kPerCu);
+  const int hold = T::hold((ntiles + grid - 1) / grid);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(T::kThreads), T::kOut + G * hold * 1024, s, A, as, M, W, ws, N, K,
+                     C, hold);
   return hipGetLastError();
 }
 
-// M <= 64 parts rows
+// M <= 64
 template <int S, int NW>
 static hipError_t launch_stream(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
-                                float* C, int parts, int num_cu, hipStream_t s) {
-  const int groups = ((M + parts - 1) / parts + 15) / 16;
-  switch (groups) {
-    case 1: return launch_stream_g<S, NW, 1>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
-    case 2: return launch_stream_g<S, NW, 2>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
-    case 3: return launch_stream_g<S, NW, 3>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
-    default: return launch_stream_g<S, NW, 4>(A, as, M, W, ws, N, K, C, parts, num_cu, s);
+                                float* C, int num_cu, hipStream_t s) {
+  switch ((M + 15) / 16) {
+    case 1: return launch_stream_g<S, NW, 1>(A, as, M, W, ws, N, K, C, num_cu, s);
+    case 2: return launch_stream_g<S, NW, 2>(A, as, M, W, ws, N, K, C, num_cu, s);
+    case 3: return launch_stream_g<S, NW, 3>(A, as, M, W, ws, N, K, C, num_cu, s);
+    default: return launch_stream_g<S, NW, 4>(A, as, M, W, ws, N, K, C, num_cu, s);
   }
 }
 
@@ -242,13 +232,19 @@ static hipError_t launch_stream(const int8_t* A, const float* as, int M, const i
 // tile are in flight while the last one's results are stored.
 // Operands go from memory straight into LDS (16 bytes a lane), in steps of 128
 // bytes of K: a load instruction covers whole 128-byte lines of 8 rows.  W and
-// A have rings of WS and 2 steps; W's, which comes from HBM, is the deeper.  The
+// A have rings of WS and AS steps.  The
 // first row of waves loads W and the second A: loads are counted back in the
 // order of their issue, and a wave that loaded both would wait for W's later
 // steps whenever it waits for A's next one.
 // Chunk c of a 128-byte LDS row r sits in slot c ^ (r & 7): a 16-byte read is
 // served 8 lanes at a time, and the 8 lanes of a fragment read (8 rows, one
 // chunk) then touch 8 different groups of banks.
+// W's loads are non-temporal, which leaves the L2 to A (128 rows of a Qwen3-8B
+// head: 189 -> 172 us).  With one M tile, N tiles begin at different steps of K
+// and wrap around (the sums are exact in any order): rows of W that lie a power
+// of two apart are then not all read at the same offset, that is from the same
+// memory channels, at a time (172 -> 149 us; with several M tiles, which share
+// W in the L2, 353 -> 361 us at 512 rows: not done).
 // The two rows of waves alternate, one phase apart: one reads the fragments of
 // half a step (64 bytes of K) and issues loads while the other multiplies,
 // with a barrier between phases.  Order: the loads into a slot are issued one
@@ -262,26 +258,26 @@ typedef __attribute__((address_space(3))) void* lptr_t;
 
 __device__ const unsigned char kZeros[16] = {};  // what A reads past K
 
-template <int BM, int WS>
+template <int BM, int WS, int AS>
 struct TileI8 {
   static constexpr int kThreads = 512, kBN = 256, kRow = 128;
   static constexpr int kABytes = BM * kRow, kWBytes = kBN * kRow;
-  static constexpr int kLds = WS * kWBytes + 2 * kABytes;
+  static constexpr int kLds = WS * kWBytes + AS * kABytes;
   static constexpr int kAL = BM / 32, kWL = kBN / 32;  // loads of a step per loading wave
   static constexpr int kFA = BM / 2 / 16, kFW = kBN / 4 / 16;
-  static_assert(BM % 128 == 0 && WS >= 3 && (WS - 2) * kWL < 64, "rings");
+  static_assert(BM % 128 == 0 && WS >= 2 && AS >= 2 && (WS - 2) * kWL < 64 && (AS - 2) * kAL < 64, "rings");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 // vmcnt(n), lgkmcnt(0); expcnt at its maximum
 #define DOMINO_I8_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | 0x0070)
 
-template <int BM, int WS>
+template <int BM, int WS, int AS>
 __global__ void __launch_bounds__(512, 1)
     gemm_i8_tiled_kernel(const int8_t* __restrict__ A, const float* __restrict__ as, int M,
                          const int8_t* __restrict__ W, const float* __restrict__ ws, int N, int K,
                          float* __restrict__ C, int num_m, int num_n) {
-  using T = TileI8<BM, WS>;
+  using T = TileI8<BM, WS, AS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, col = lane & 15;
   const int wm = wave >> 2, wn = wave & 3;
@@ -309,23 +305,26 @@ __global__ void __launch_bounds__(512, 1)
   const int8_t* base = A;  // the tile's first row
   int last_row = 0;        // the operand's last row, counted from it
   int it = 0, id = 0, islot = 0;  // the next step to load: tile, step, ring slot
+  int turn = 0;                   // the step of K that the tile begins with
   auto seek = [&]() {
     int m0, n0;
     tile_at(it, m0, n0);
     const int r0 = loads_w ? n0 : m0, rows = loads_w ? N : M;
     base = (loads_w ? W : A) + (size_t)r0 * K;
     last_row = rows - 1 - r0;
+    turn = num_m == 1 ? (int)((unsigned)(n0 / T::kBN * 5) % (unsigned)nd) : 0;
   };
   auto issue = [&]() {
-    const bool skip = past && id == nd - 1;
-    const int8_t* p = base + id * 128;
+    const int kd = id + turn < nd ? id + turn : id + turn - nd;
+    const bool skip = past && kd == nd - 1;
+    const int8_t* p = base + kd * 128;
     const uint32_t c16 = chunk * 16;
     if (loads_w) {
       unsigned char* dst = smem + islot * T::kWBytes + (wave & 3) * 1024;
 #pragma unroll
       for (int i = 0; i < T::kWL; ++i)
         __builtin_amdgcn_global_load_lds((gptr_t)(p + (uint32_t)(min(i * 32 + lrow, last_row) * K) + (skip ? 0 : c16)),
-                                         (lptr_t)(dst + i * 4096), 16, 0, 0);
+                                         (lptr_t)(dst + i * 4096), 16, 0, kLoadNonTemporal);
       if (++islot == WS) islot = 0;
     } else {
       unsigned char* dst = smem + WS * T::kWBytes + islot * T::kABytes + (wave & 3) * 1024;
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(512, 1)
         if (skip) q = kZeros;
         __builtin_amdgcn_global_load_lds((gptr_t)q, (lptr_t)(dst + i * 4096), 16, 0, 0);
       }
-      islot ^= 1;
+      if (++islot == AS) islot = 0;
     }
     if (++id == nd) {
       id = 0;
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(512, 1)
   };
 
   seek();
-  const int ahead = loads_w ? WS - 1 : 1;
+  const int ahead = loads_w ? WS - 1 : AS - 1;
   for (int q = 0; q < ahead; ++q)
     if (q < total) issue();
   DOMINO_I8_WAIT(0);
@@ -440,6 +439,8 @@ __global__ void __launch_bounds__(512, 1)
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       } else if (loads_w && g + WS - 1 < total) {
         DOMINO_I8_WAIT((WS - 2) * T::kWL);
+      } else if (!loads_w && g + AS - 1 < total) {
+        DOMINO_I8_WAIT((AS - 2) * T::kAL);
       } else {
         DOMINO_I8_WAIT(0);
       }
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(512, 1)
       if (h == 1 && d == nd - 1) store();
       __builtin_amdgcn_s_barrier();
     }
-    sa_slot ^= 1;
+    if (++sa_slot == AS) sa_slot = 0;
     if (++sw_slot == WS) sw_slot = 0;
     if (++d == nd) {
       d = 0;
@@ -465,14 +466,14 @@ __global__ void __launch_bounds__(512, 1)
   if (wm == 0) __builtin_amdgcn_s_barrier();  // equal barrier counts in both rows of waves
 }
 
-template <int BM, int WS>
+template <int BM, int WS, int AS>
 static hipError_t launch_tiled(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
                                float* C, int num_cu, hipStream_t s) {
-  using T = TileI8<BM, WS>;
+  using T = TileI8<BM, WS, AS>;
   const int num_m = (M + BM - 1) / BM, num_n = (N + T::kBN - 1) / T::kBN;
   // a multiple of 8 workgroups, at most one a compute unit
   const int want = (num_n + 7) / 8 * num_m, have = std::max(1, num_cu / 8);
-  auto kern = gemm_i8_tiled_kernel<BM, WS>;
+  auto kern = gemm_i8_tiled_kernel<BM, WS, AS>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), T::kLds, done);
   if (e != hipSuccess) return e;
@@ -485,18 +486,20 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
                           int K, float* C, int num_cu, hipStream_t s) {
   if (M <= 0 || N <= 0) return hipSuccess;
   if (K <= 0 || K % 32 || K > 8192) return hipErrorNotSupported;
-  const int parts = (M + 63) / 64;
-  if (K <= 4096 && parts <= 2) {
-    if (K <= 256) return launch_stream<4, 1>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
-    if (K <= 512) return launch_stream<4, 2>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
-    if (K <= 1024) return launch_stream<4, 4>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
-    if (K <= 2048) return launch_stream<4, 8>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
-    if (K <= 2560) return launch_stream<5, 8>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
-    return launch_stream<8, 8>(A, a_scale, M, W, w_scale, N, K, C, parts, num_cu, s);
+  // Up to 64 rows W is streamed past A in registers (Qwen3-8B head, 64 rows:
+  // 118 us against 170 tiled); above, two workgroups would share each stream
+  // (128 rows: 160 us, against 149 tiled).
+  if (M <= 64 && K <= 4096) {
+    if (K <= 256) return launch_stream<4, 1>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+    if (K <= 512) return launch_stream<4, 2>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+    if (K <= 1024) return launch_stream<4, 4>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+    if (K <= 2048) return launch_stream<4, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+    if (K <= 2560) return launch_stream<5, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+    return launch_stream<8, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
   }
-  if (M <= 16) return launch_stream_g<16, 8, 1>(A, a_scale, M, W, w_scale, N, K, C, 1, num_cu, s);
-  return M <= 128 ? launch_tiled<128, 4>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
-                  : launch_tiled<256, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  if (M <= 16) return launch_stream_g<16, 8, 1>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  return M <= 128 ? launch_tiled<128, 3, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
+                  : launch_tiled<256, 2, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
 }
 
 }  // namespace domino
