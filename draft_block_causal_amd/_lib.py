@@ -108,6 +108,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P, I32, U32, U64, SZ, F = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64,
                                ctypes.c_size_t, ctypes.c_float)
+    F64 = ctypes.c_double
     HP = ctypes.POINTER(DominoHeadStruct)
     sig = {
         "domino_version": (ctypes.c_int, []),
@@ -133,9 +134,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "domino_gru_backward_workspace_size": (ctypes.c_int, [HP, I32, ctypes.POINTER(SZ)]),
         "domino_quantize_rows": (ctypes.c_int, [I32, I32, I32, P, P, P, P]),
         "domino_base_logits_i8": (ctypes.c_int, [I32, I32, I32, I32, P, P, P, P, P, P]),
-        "domino_token_logprobs": (ctypes.c_int, [I32, I32, I32, P, P, P, F, P, P, P, SZ, P]),
+        "domino_token_logprobs": (ctypes.c_int, [I32, I32, I32, P, P, P, F64, P, P, P, SZ, P]),
         "domino_token_logprobs_workspace_size": (SZ, [I32, I32, I32]),
-        "domino_policy_loss": (ctypes.c_int, [I32, I32, I32, P, P, P, P, P, P, F, F, F, F, P, P, P, P, P, SZ, P]),
+        "domino_policy_loss": (ctypes.c_int, [I32, I32, I32, P, P, P, P, P, P, F64, F64, F64, F64, P, P, P, P, P, SZ, P]),
         "domino_policy_loss_workspace_size": (SZ, [I32, I32, I32]),
         "domino_debug_read_stream": (ctypes.c_int, [P, SZ, P, P]),
         "domino_debug_philox": (ctypes.c_int, [U64, U32, I32, I32, I32, I32, P, P]),

@@ -351,7 +351,7 @@ extern "C" size_t domino_policy_loss_workspace_size(int32_t batch, int32_t block
 }
 
 extern "C" int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float* logits,
-                                     const int32_t* tokens, const float* weights, float temperature, float* logp,
+                                     const int32_t* tokens, const float* weights, double temperature, float* logp,
                                      float* entropy, void* workspace, size_t workspace_bytes, void* stream) {
   int st = domino::check_logprobs_args(batch, block, vocab, logits, tokens, weights, temperature, logp, entropy,
                                        workspace, workspace_bytes);
@@ -363,14 +363,16 @@ extern "C" int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab
 
 extern "C" int domino_policy_loss(int32_t batch, int32_t block, int32_t vocab, const float* logits,
                                   const int32_t* tokens, const float* old_logp, const float* ref_logp,
-                                  const float* advantages, const float* weights, float temperature, float clip_low,
-                                  float clip_high, float kl_coef, float* loss, float* logp, float* kl, float* grad,
+                                  const float* advantages, const float* weights, double temperature, double clip_low,
+                                  double clip_high, double kl_coef, float* loss, float* logp, float* kl, float* grad,
                                   void* workspace, size_t workspace_bytes, void* stream) {
   const domino::PolicyArgs a{batch,    block,       vocab,    logits,    tokens,  old_logp, ref_logp, advantages, weights,
                              temperature, clip_low, clip_high, kl_coef, loss,     logp,     kl,       grad};
   int st = domino::check_policy_args(a, workspace, workspace_bytes);
   if (st != DOMINO_OK || batch == 0) return st;
-  return hip_status(domino::launch_policy_loss(a, domino::policy_plan(batch, block, vocab), workspace,
+  const int num_cu = device_cu_count();
+  if (num_cu <= 0) return DOMINO_ERR_HIP;
+  return hip_status(domino::launch_policy_loss(a, domino::policy_plan(batch, block, vocab), workspace, num_cu,
                                                static_cast<hipStream_t>(stream)));
 }
 

@@ -377,9 +377,10 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
 // Drafted-token log-probabilities and the clipped policy loss (policy.hip);
 // the workspace follows policy_plan(B, K, V).
 hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
-                                 float temperature, float* logp, float* entropy, const PolicyPlan& plan,
+                                 double temperature, float* logp, float* entropy, const PolicyPlan& plan,
                                  void* workspace, hipStream_t s);
-hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void* workspace, hipStream_t s);
+hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void* workspace, int num_cu,
+                              hipStream_t s);
 
 hipError_t launch_accept_len(int B, int K, const int32_t* draft, const int32_t* target, int32_t* accept,
                              hipStream_t s);

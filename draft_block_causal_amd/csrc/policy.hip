@@ -1,27 +1,35 @@
 // Log-probabilities of drafted tokens, and the clipped policy loss with its
 // gradient with respect to the logits.
 //
-// For a row x of V logits with maximum M, in base-2 units t_v = c (x_v - M),
-// c = log2(e) / T:  s = sum 2^t_v,  u = sum 2^t_v t_v,
-//     logp = (x_y - M) / T - ln s,   entropy = ln s - ln 2 u / s,
+// For a row x of V logits with maximum M, in base-2 units t_v = c x_v - R,
+// c = log2(e) / T, R an integer near c M:  s = sum 2^t_v,  u = sum 2^t_v t_v,
+//     logp = ln 2 (c x_y - R) - ln s,   entropy = ln s - ln 2 u / s,
 //     grad_v = coef (1[v = y] - 2^t_v / s),
 // where coef is the loss's derivative with respect to logp times w / T.
+// R is an integer so that sums over different references are brought together
+// by exact factors; t_v is one fused product (and a second one for the part of
+// c below float32), so it is off by |t_v| 2^-24 at most, and the terms that make
+// up s have |t_v| of order 1.  R is exact and t_v finite while |c M| < 2^30; a row
+// outside (a mask value in every entry, say) is taken again with t_v = c (x_v - M).
+// What a row has one of (ln s, the ratio, the divergence, the loss) is in
+// float64: a divergence is a small difference of numbers near 10.
 //
-// Launches on the caller's stream, grids over (row, vocabulary slice):
-//   1. policy_stats_kernel: (M, s, u) of one slice, and the token's logit;
-//   2. logprobs_rows_kernel: a thread per row merges the slices; or
-//      policy_grad_kernel: each workgroup merges its row's slices again (at
-//      most 32), forms coef and writes its slice of the gradient; workgroup 0
-//      takes every row's logp, kl and loss term and the sum, so that neither
-//      needs a launch of its own.
-// Bound by HBM: V floats read in pass 1, V read and V written in pass 2.
-//
-// Everything a row has one of (ln s, the ratio, the divergence, the loss) is
-// in float64: a divergence is a small difference of numbers near 10.  c is
-// applied as a float32 pair, since its rounding would shift every term of s
-// the same way (3e-8 |x - M| / T of s; the errors of the terms themselves
-// average out).
+// Launches on the caller's stream:
+//   policy_held_kernel, a workgroup per row, for as many rows as make whole
+//     rounds over the compute units: the row is read once and held on chip
+//     (registers, and LDS for the longest) between its sum and its gradient;
+//   policy_stats_kernel, a workgroup per (row, vocabulary slice), for the other
+//     rows, for calls without a gradient and for the log-probabilities;
+//   logprobs_rows_kernel, a thread per row: merges the slices; or
+//   policy_grad_kernel, a workgroup per (row, slice): merges its row's slices
+//     again (at most 32), forms coef and writes its slice of the gradient;
+//     workgroup 0 takes the rows' logp, kl and loss terms and the loss, so that
+//     neither needs a launch of its own.
+// Bound by HBM: a row's logits once in and its gradient once out (held), or
+// twice in and once out.
 #include <math.h>
+
+#include <algorithm>
 
 #include "common.h"
 #include "kernels.h"
@@ -31,30 +39,44 @@ namespace domino {
 constexpr int kPolThreads = 256;
 constexpr int kPolWaves = kPolThreads / 64;
 
-// log2(e) / T as a float32 pair
+// log2(e) / T as a float32 pair with 0 < lo (so that x = -inf stays -inf)
 struct Base2 {
   float hi, lo;
 };
 
+// Maximum of some logits (the exact one), and sums relative to R(m).  The sums
+// are in float64, added to by float32 sums of 16 terms: one term near 1 would
+// swallow the last bits of hundreds of small ones (2e-6 of a divergence).
 struct SoftPart {
-  float m, s, u;
+  float m;
+  double s, u;
 };
 
-// 2^(c (x - m)): also for x = -inf (the low product is kept finite, which
-// leaves a NaN to the high one).
-__device__ __forceinline__ float base2(float x, float m, Base2 c) {
-  const float d = x - m;
-  return fmaf(d, c.hi, fmaxf(d, -3.0e38f) * c.lo);
+__device__ __forceinline__ float exp2_hw(float t) { return __builtin_amdgcn_exp2f(t); }
+
+constexpr float kRefMax = 1073741824.f;  // 2^30
+__device__ __forceinline__ float ref_of(float m, Base2 c) {
+  return fminf(fmaxf(rintf(m * c.hi), -kRefMax), kRefMax);
+}
+// Whether a row's maximum lies where R(m) does not serve (not: no entry at all).
+__device__ __forceinline__ bool far_out(float m, Base2 c) { return m != -INFINITY && !(fabsf(m * c.hi) < kRefMax); }
+
+// t relative to R
+__device__ __forceinline__ float base2(float x, float R, Base2 c) { return fmaf(x, c.lo, fmaf(x, c.hi, -R)); }
+
+// p relative to R(m), m >= p.m
+__device__ __forceinline__ SoftPart soft_to(SoftPart p, float m, Base2 c) {
+  const float d = ref_of(p.m, c) - ref_of(m, c);
+  const int e = (int)fmaxf(d, -4096.f);
+  const double s = ldexp(p.s, e);
+  return SoftPart{m, s, fma((double)e, s, ldexp(p.u, e))};
 }
 
 __device__ __forceinline__ SoftPart soft_merge(SoftPart a, SoftPart b, Base2 c) {
-  if (a.m == -INFINITY) return b;
-  if (b.m == -INFINITY) return a;
   const float m = fmaxf(a.m, b.m);
-  const float ta = base2(a.m, m, c), tb = base2(b.m, m, c);
-  const float ea = __builtin_amdgcn_exp2f(ta), eb = __builtin_amdgcn_exp2f(tb);
-  return SoftPart{m, ea * a.s + eb * b.s,
-                  ea * (a.u + fmaxf(ta, -200.f) * a.s) + eb * (b.u + fmaxf(tb, -200.f) * b.s)};
+  a = soft_to(a, m, c);
+  b = soft_to(b, m, c);
+  return SoftPart{m, a.s + b.s, a.u + b.u};
 }
 
 __device__ __forceinline__ SoftPart wave_soft(SoftPart p, Base2 c) {
@@ -66,29 +88,38 @@ __device__ __forceinline__ SoftPart wave_soft(SoftPart p, Base2 c) {
   return p;
 }
 
-// Folds n values into a running part; values of -inf add nothing, a NaN or
-// +inf makes s NaN.
+constexpr SoftPart kNone{-INFINITY, 0.0, 0.0};
+
+// Folds N values into a running part whose reference R = R(p.m) is kept along.
+// Values of -inf add nothing; a NaN makes s NaN.
 template <int N, bool ENT>
-__device__ __forceinline__ void soft_add(SoftPart& p, const float (&x)[N], Base2 c) {
+__device__ __forceinline__ void soft_add(SoftPart& p, float& R, const float (&x)[N], Base2 c) {
   float top = x[0];
 #pragma unroll
   for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
   if (top > p.m) {
-    if (p.m != -INFINITY) {
-      const float t = base2(p.m, top, c), f = __builtin_amdgcn_exp2f(t);
-      if (ENT) p.u = f * (p.u + fmaxf(t, -200.f) * p.s);
-      p.s *= f;
-    }
-    p.m = top;
+    p = soft_to(p, top, c);
+    R = ref_of(top, c);
   }
-  const float m = p.m == -INFINITY ? 0.f : p.m;
+  float f[N], g[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const float t = base2(x[e], m, c), f = __builtin_amdgcn_exp2f(t);
-    p.s += f;
-    if (ENT) p.u = fmaf(f, fmaxf(t, -200.f), p.u);
+    const float t = base2(x[e], R, c);
+    f[e] = exp2_hw(t);
+    if (ENT) g[e] = f[e] * fmaxf(t, -200.f);
   }
+#pragma unroll
+  for (int h = N / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int e = 0; e < h; ++e) {
+      f[e] += f[e + h];
+      if (ENT) g[e] += g[e + h];
+    }
+  p.s += (double)f[0];
+  if (ENT) p.u += (double)g[0];
 }
+
+__device__ __forceinline__ int clamp_id(int y, int V) { return min(max(y, 0), V - 1); }
 
 // Entries [v0, v1) of slice s of S of a row of V at `row`: inner boundaries
 // fall on 16-byte boundaries of the row's own memory.
@@ -99,70 +130,130 @@ __device__ __forceinline__ void row_slice(const float* row, int V, int s, int S,
   v1 = s == S - 1 ? V : head + 4 * (int)(n4 * (s + 1) / S);
 }
 
-__device__ __forceinline__ int clamp_id(int y, int V) { return min(max(y, 0), V - 1); }
+// The whole 16-byte groups of entries v0 .. v1 - 1 (a4 .. b4 - 1), and the at
+// most 6 entries outside them: outer entry e, e < outer.
+struct Span {
+  int v0, v1, a4, b4, n4, outer;
+  __device__ __forceinline__ Span(const float* row, int v0_, int v1_) : v0(v0_), v1(v1_) {
+    a4 = min(v1, v0 + ((int)((16 - (reinterpret_cast<uintptr_t>(row + v0) & 15)) & 15) >> 2));
+    b4 = a4 + ((v1 - a4) & ~3);
+    n4 = (b4 - a4) >> 2;
+    outer = (a4 - v0) + (v1 - b4);
+  }
+  __device__ __forceinline__ int outer_at(int e) const { return e < a4 - v0 ? v0 + e : b4 + e - (a4 - v0); }
+  // The thread of NT that handles entry v (groups are dealt out in turn).
+  __device__ __forceinline__ int owner(int v, int NT) const {
+    return v < a4 ? v - v0 : v < b4 ? ((v - a4) >> 2) % NT : (a4 - v0) + v - b4;
+  }
+};
 
-// Entries v0 .. a4 - 1 and b4 .. v1 - 1 of a slice lie outside its whole
-// 16-byte groups.
-__device__ __forceinline__ void slice_vectors(const float* row, int v0, int v1, int& a4, int& b4) {
-  a4 = min(v1, v0 + ((int)((16 - (reinterpret_cast<uintptr_t>(row + v0) & 15)) & 15) >> 2));
-  b4 = a4 + ((v1 - a4) & ~3);
+// A workgroup's part from its waves' parts; the result in every thread of wave
+// 0 at least.  red: one entry per wave.
+template <int WAVES>
+__device__ __forceinline__ SoftPart block_soft(SoftPart p, SoftPart* red, Base2 c) {
+  p = wave_soft(p, c);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = p;
+  __syncthreads();
+  p = red[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) p = soft_merge(p, red[w], c);
+  return p;
+}
+
+// Sums of a far-out slice with maximum m, t = c (x - m).  Every thread of the
+// workgroup calls it (red: one entry per wave, not in use).
+template <int WAVES>
+__device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 c, SoftPart* red) {
+  double s = 0.0, u = 0.0;
+  for (int v = v0 + threadIdx.x; v < v1; v += WAVES * 64) {
+    const float t = (x[v] - m) * c.hi, f = exp2_hw(t);
+    s += (double)f;
+    u += (double)(f * fmaxf(t, -200.f));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    s += __shfl_xor(s, o);
+    u += __shfl_xor(u, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = SoftPart{m, s, u};
+  __syncthreads();
+  SoftPart p = red[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) {
+    p.s += red[w].s;
+    p.u += red[w].u;
+  }
+  return p;
 }
 
 template <bool ENT>
 __global__ void __launch_bounds__(kPolThreads)
-    policy_stats_kernel(int V, int S, Base2 c, const float* __restrict__ logits, const int32_t* __restrict__ tokens,
-                        const float* __restrict__ weights, float4* __restrict__ stats, float* __restrict__ xy) {
+    policy_stats_kernel(int row0, int V, int S, Base2 c, const float* __restrict__ logits,
+                        const int32_t* __restrict__ tokens, const float* __restrict__ weights,
+                        SoftPart* __restrict__ stats, float* __restrict__ xy) {
   __shared__ SoftPart red[kPolWaves];
-  const int row = blockIdx.x, sl = blockIdx.y;
+  const int row = row0 + blockIdx.x, sl = blockIdx.y;
   if (weights && weights[row] == 0.f) return;
   const float* x = logits + (size_t)row * V;
-  int v0, v1, a4, b4;
+  int v0, v1;
   row_slice(x, V, sl, S, v0, v1);
-  slice_vectors(x, v0, v1, a4, b4);
-  SoftPart p{-INFINITY, 0.f, 0.f};
-  const float4* x4 = reinterpret_cast<const float4*>(x + a4);
-  const int n4 = (b4 - a4) >> 2;
+  const Span sp(x, v0, v1);
+  SoftPart p = kNone;
+  float R = ref_of(p.m, c);
+  const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
   int q = threadIdx.x;
-  for (; q + 3 * kPolThreads < n4; q += 4 * kPolThreads) {
-    const float4 f0 = x4[q], f1 = x4[q + kPolThreads], f2 = x4[q + 2 * kPolThreads], f3 = x4[q + 3 * kPolThreads];
-    const float f[16] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w,
-                         f2.x, f2.y, f2.z, f2.w, f3.x, f3.y, f3.z, f3.w};
-    soft_add<16, ENT>(p, f, c);
+  for (; q + 3 * kPolThreads < sp.n4; q += 4 * kPolThreads) {
+    f32x4 f4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f4[i] = x4[q + i * kPolThreads];
+    float f[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = f4[e >> 2][e & 3];
+    soft_add<16, ENT>(p, R, f, c);
   }
-  for (; q < n4; q += kPolThreads) {
-    const float4 f0 = x4[q];
-    const float f[4] = {f0.x, f0.y, f0.z, f0.w};
-    soft_add<4, ENT>(p, f, c);
+  for (; q < sp.n4; q += kPolThreads) {
+    const f32x4 f0 = x4[q];
+    const float f[4] = {f0[0], f0[1], f0[2], f0[3]};
+    soft_add<4, ENT>(p, R, f, c);
   }
-  const int outer = (a4 - v0) + (v1 - b4);  // at most 6
-  if ((int)threadIdx.x < outer) {
-    const int e = threadIdx.x, v = e < a4 - v0 ? v0 + e : b4 + e - (a4 - v0);
-    const float f[1] = {x[v]};
-    soft_add<1, ENT>(p, f, c);
+  if ((int)threadIdx.x < sp.outer) {
+    const float f[1] = {x[sp.outer_at(threadIdx.x)]};
+    soft_add<1, ENT>(p, R, f, c);
   }
-  p = wave_soft(p, c);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = p;
-  __syncthreads();
+  p = block_soft<kPolWaves>(p, red, c);
+  if (far_out(p.m, c)) p = far_out_part<kPolWaves>(x, v0, v1, p.m, c, red);
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kPolWaves; ++w) p = soft_merge(p, red[w], c);
-    stats[(size_t)row * S + sl] = float4{p.m, p.s, p.u, 0.f};
+    stats[(size_t)row * S + sl] = p;
     const int y = clamp_id(tokens[row], V);
     if (y >= v0 && y < v1) xy[row] = x[y];
   }
 }
 
-// One row's statistics, its slices merged in order.
-__device__ __forceinline__ SoftPart row_part(const float4* __restrict__ stats, int row, int S, Base2 c) {
-  SoftPart p{-INFINITY, 0.f, 0.f};
-  for (int q = 0; q < S; ++q) {
-    const float4 f = stats[(size_t)row * S + q];
-    p = soft_merge(p, SoftPart{f.x, f.y, f.z}, c);
-  }
+// Slices in order.  (A far-out slice below a maximum that is not adds nothing.)
+__device__ __forceinline__ SoftPart slice_merge(SoftPart a, SoftPart b, Base2 c) {
+  const float m = fmaxf(a.m, b.m);
+  if (!far_out(m, c)) return soft_merge(a, b, c);
+  const float ta = a.m == -INFINITY ? -INFINITY : (a.m - m) * c.hi, tb = b.m == -INFINITY ? -INFINITY : (b.m - m) * c.hi;
+  const float ea = exp2_hw(ta), eb = exp2_hw(tb);
+  return SoftPart{m, ea * a.s + eb * b.s,
+                  ea * (a.u + fmaxf(ta, -200.f) * a.s) + eb * (b.u + fmaxf(tb, -200.f) * b.s)};
+}
+
+// ln of the row's sum with the part of logp before it: logp = shift(x_y) - ln s.
+__device__ __forceinline__ double shift_of(float xy, const SoftPart& p, Base2 c, double inv_t) {
+  if (far_out(p.m, c)) return ((double)xy - (double)p.m) * inv_t;
+  return (double)xy * inv_t - 0.6931471805599453 * (double)ref_of(p.m, c);
+}
+
+__device__ __forceinline__ SoftPart row_part(const SoftPart* stats, int row, int S, Base2 c) {
+  SoftPart p = stats[(size_t)row * S];
+  for (int q = 1; q < S; ++q) p = slice_merge(p, stats[(size_t)row * S + q], c);
   return p;
 }
 
 __global__ void __launch_bounds__(kPolThreads)
-    logprobs_rows_kernel(int rows, int S, Base2 c, double inv_t, const float4* __restrict__ stats,
+    logprobs_rows_kernel(int rows, int S, Base2 c, double inv_t, const SoftPart* __restrict__ stats,
                          const float* __restrict__ xy, const float* __restrict__ weights, float* __restrict__ logp,
                          float* __restrict__ entropy) {
   const int row = blockIdx.x * kPolThreads + threadIdx.x;
@@ -170,12 +261,12 @@ __global__ void __launch_bounds__(kPolThreads)
   float lp = 0.f, h = 0.f;
   if (!(weights && weights[row] == 0.f)) {
     const SoftPart p = row_part(stats, row, S, c);
-    if (p.m == -INFINITY) {
+    if (p.s == 0.0) {
       lp = -INFINITY;
     } else {
-      const double ln_s = log((double)p.s);
-      lp = (float)(((double)xy[row] - (double)p.m) * inv_t - ln_s);
-      h = (float)(ln_s - 0.6931471805599453 * ((double)p.u / (double)p.s));
+      const double ln_s = log(p.s);
+      lp = (float)(shift_of(xy[row], p, c, inv_t) - ln_s);
+      h = (float)(ln_s - 0.6931471805599453 * (p.u / p.s));
     }
   }
   logp[row] = lp;
@@ -183,25 +274,26 @@ __global__ void __launch_bounds__(kPolThreads)
 }
 
 struct PolicyDev {
-  int rows, V, S;
+  int rows, held, V, S;  // rows below `held` are the held kernel's
   Base2 c;
   double inv_t, lo, hi, beta;  // clip range limits; KL coefficient
   const float *logits, *old_logp, *ref_logp, *advantages, *weights;
   const int32_t* tokens;
-  const float4* stats;
+  const SoftPart* stats;
   const float* xy;
+  double* terms;  // [held] weighted loss terms
   float *loss, *logp, *kl, *grad;
 };
 
 struct RowTerms {
   float logp, kl;
-  double term, coef;  // weighted loss term; derivative with respect to the row's logit of the token (1 - p_y aside)
+  double term, coef;  // weighted loss term; its derivative with respect to logp, over T
 };
 
-__device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, SoftPart p) {
+__device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, float xy, const SoftPart& p) {
   RowTerms r{-INFINITY, 0.f, 0.0, 0.0};
-  if (p.m == -INFINITY) return r;  // no distribution
-  const double lp = ((double)a.xy[row] - (double)p.m) * a.inv_t - log((double)p.s);
+  if (p.s == 0.0) return r;  // no distribution
+  const double lp = shift_of(xy, p, a.c, a.inv_t) - log(p.s);
   const double w = a.weights ? (double)a.weights[row] : 1.0 / a.rows;
   const double adv = a.advantages[row], ratio = exp(lp - (double)a.old_logp[row]);
   const bool inside = adv >= 0.0 ? ratio <= a.hi : ratio >= a.lo;
@@ -227,14 +319,19 @@ __device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, SoftP
   return r;
 }
 
-// Workgroup 0: every row's logp and kl, and the loss, each thread adding rows
-// t, t + 256, ... in order and a fixed tree over the threads' sums.
+// Workgroup 0 of policy_grad_kernel: logp and kl of the rows that are not held,
+// and the loss, each thread adding rows t, t + 256, ... in order and a fixed tree
+// over the threads' sums.
 __device__ void policy_rows(const PolicyDev& a) {
   __shared__ double part[kPolThreads];
   double acc = 0.0;
   for (int row = threadIdx.x; row < a.rows; row += kPolThreads) {
+    if (row < a.held) {
+      acc += a.terms[row];
+      continue;
+    }
     RowTerms r{0.f, 0.f, 0.0, 0.0};
-    if (!(a.weights && a.weights[row] == 0.f)) r = row_terms(a, row, row_part(a.stats, row, a.S, a.c));
+    if (!(a.weights && a.weights[row] == 0.f)) r = row_terms(a, row, a.xy[row], row_part(a.stats, row, a.S, a.c));
     if (a.logp) a.logp[row] = r.logp;
     if (a.kl) a.kl[row] = r.kl;
     acc += r.term;
@@ -248,133 +345,281 @@ __device__ void policy_rows(const PolicyDev& a) {
   if (threadIdx.x == 0) a.loss[0] = (float)part[0];
 }
 
+// What a row's gradient is made of: grad = k 2^t (+ coef at the token).
+struct GradRow {
+  float ref, k, coef;  // ref: R, or the maximum of a far-out row
+  int far;
+};
+
+__device__ __forceinline__ GradRow grad_row(const RowTerms& r, const SoftPart& p, Base2 c) {
+  const bool far = far_out(p.m, c);
+  return GradRow{far ? p.m : ref_of(p.m, c), r.coef == 0.0 ? 0.f : (float)(-r.coef / p.s), (float)r.coef, far};
+}
+
+__device__ __forceinline__ float grad_of(float x, const GradRow& g, Base2 c) {
+  const float t = g.far ? (x - g.ref) * c.hi : base2(x, g.ref, c);
+  return g.k * exp2_hw(t);
+}
+
+__device__ __forceinline__ f32x4 grad_of4(f32x4 x, const GradRow& g, Base2 c) {
+  return f32x4{grad_of(x[0], g, c), grad_of(x[1], g, c), grad_of(x[2], g, c), grad_of(x[3], g, c)};
+}
+
+template <int NT>
+__device__ __forceinline__ void zero_span(float* g, const Span& sp) {
+  for (int q = threadIdx.x; q < sp.n4; q += NT) *reinterpret_cast<f32x4*>(g + sp.a4 + 4 * q) = f32x4{0.f, 0.f, 0.f, 0.f};
+  if ((int)threadIdx.x < sp.outer) g[sp.outer_at(threadIdx.x)] = 0.f;
+}
+
+// (x and g may be the same buffer: every entry is read by the thread that
+// writes it, before it does, and the token's logit comes from xy)
 __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
   if (blockIdx.x == 0) {
     policy_rows(a);
     return;
   }
-  __shared__ float sh[3];
+  __shared__ GradRow sh;
   const unsigned b = blockIdx.x - 1;
-  const int row = (int)(b / (unsigned)a.S), sl = (int)(b % (unsigned)a.S);
-  float m = 0.f, k = 0.f, coef = 0.f;
-  if (!(a.weights && a.weights[row] == 0.f)) {
-    if (threadIdx.x < 64) {
-      // each lane takes one slice (S <= 32)
-      const int q = threadIdx.x;
-      SoftPart p{-INFINITY, 0.f, 0.f};
-      if (q < a.S) {
-        const float4 f = a.stats[(size_t)row * a.S + q];
-        p = SoftPart{f.x, f.y, f.z};
-      }
-      p = wave_soft(p, a.c);
-      if (q == 0) {
-        const RowTerms r = row_terms(a, row, p);
-        sh[0] = p.m;
-        sh[1] = r.coef == 0.0 ? 0.f : (float)(-r.coef / (double)p.s);
-        sh[2] = (float)r.coef;
-      }
-    }
-    __syncthreads();
-    m = sh[0];
-    k = sh[1];
-    coef = sh[2];
-  }
+  const int row = a.held + (int)(b / (unsigned)a.S), sl = (int)(b % (unsigned)a.S);
   const float* x = a.logits + (size_t)row * a.V;
   float* g = a.grad + (size_t)row * a.V;
-  int v0, v1, a4, b4;
+  int v0, v1;
   row_slice(x, a.V, sl, a.S, v0, v1);
-  slice_vectors(g, v0, v1, a4, b4);
-  const int y = clamp_id(a.tokens[row], a.V);
-  const int n4 = (b4 - a4) >> 2;
-  if (k == 0.f && coef == 0.f) {  // no gradient here: nothing is read
-    for (int q = threadIdx.x; q < n4; q += kPolThreads)
-      *reinterpret_cast<float4*>(g + a4 + 4 * q) = float4{0.f, 0.f, 0.f, 0.f};
-    const int outer = (a4 - v0) + (v1 - b4);
-    if ((int)threadIdx.x < outer) {
-      const int e = threadIdx.x, v = e < a4 - v0 ? v0 + e : b4 + e - (a4 - v0);
-      g[v] = 0.f;
-    }
+  const Span sp(g, v0, v1);
+  if (a.weights && a.weights[row] == 0.f) {  // nothing is read
+    zero_span<kPolThreads>(g, sp);
     return;
   }
-  auto one = [&](float xv, int v) {
-    const float e = k * __builtin_amdgcn_exp2f(base2(xv, m, a.c));
-    return v == y ? e + coef : e;
-  };
+  const float xy = a.xy[row];
+  if (threadIdx.x < 64) {
+    // each lane takes one slice (S <= 32)
+    const int q = threadIdx.x;
+    SoftPart p = kNone;
+    if (q < a.S) p = a.stats[(size_t)row * a.S + q];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const SoftPart r{__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.u, o)};
+      p = slice_merge(p, r, a.c);
+    }
+    if (q == 0) sh = grad_row(row_terms(a, row, xy, p), p, a.c);
+  }
+  __syncthreads();
+  const GradRow gr = sh;
+  if (gr.k == 0.f && gr.coef == 0.f) {  // nor here
+    zero_span<kPolThreads>(g, sp);
+    return;
+  }
+  const int y = clamp_id(a.tokens[row], a.V);
   if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0) {
-    for (int q = threadIdx.x; q < n4; q += kPolThreads) {
-      const int v = a4 + 4 * q;
-      const float4 f = *reinterpret_cast<const float4*>(x + v);
-      *reinterpret_cast<float4*>(g + v) = float4{one(f.x, v), one(f.y, v + 1), one(f.z, v + 2), one(f.w, v + 3)};
+    for (int q = threadIdx.x; q < sp.n4; q += kPolThreads) {
+      const int v = sp.a4 + 4 * q;
+      *reinterpret_cast<f32x4*>(g + v) = grad_of4(*reinterpret_cast<const f32x4*>(x + v), gr, a.c);
     }
-    const int outer = (a4 - v0) + (v1 - b4);
-    if ((int)threadIdx.x < outer) {
-      const int e = threadIdx.x, v = e < a4 - v0 ? v0 + e : b4 + e - (a4 - v0);
-      g[v] = one(x[v], v);
+    if ((int)threadIdx.x < sp.outer) {
+      const int v = sp.outer_at(threadIdx.x);
+      g[v] = grad_of(x[v], gr, a.c);
     }
+    // (the owner's second store to the entry, in its program order)
+    if (y >= v0 && y < v1 && (int)threadIdx.x == sp.owner(y, kPolThreads)) g[y] = grad_of(xy, gr, a.c) + gr.coef;
   } else {
-    for (int v = v0 + threadIdx.x; v < v1; v += kPolThreads) g[v] = one(x[v], v);
+    for (int v = v0 + threadIdx.x; v < v1; v += kPolThreads) {
+      const float e = grad_of(x[v], gr, a.c);
+      g[v] = v == y ? e + gr.coef : e;
+    }
   }
 }
 
-static Base2 base2_factor(float temperature) {
-  const double c = 1.4426950408889634 / (double)temperature;
-  const float hi = (float)c;
+// ---------------------------------------------------------------------------
+// Held rows: 512 threads, H groups of 4 logits a thread in registers, L more in
+// LDS (filled by loads that bypass the registers), the rest read twice.  All
+// loads of the held groups are issued at once, so a compute unit has up to 580
+// KB in flight, and the row's terms are added up as they come in.
+// ---------------------------------------------------------------------------
+constexpr int kHeldThreads = 512;
+typedef __attribute__((address_space(1))) const void* held_gptr_t;
+typedef __attribute__((address_space(3))) void* held_lptr_t;
+
+template <int H, int L>
+__global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a) {
+  constexpr int NT = kHeldThreads, WAVES = NT / 64;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  f32x4* lds = reinterpret_cast<f32x4*>(smem);  // [L][NT]
+  __shared__ SoftPart red[WAVES];
+  __shared__ GradRow sh;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const float* x = a.logits + (size_t)row * a.V;
+  float* g = a.grad + (size_t)row * a.V;
+  const Span sp(x, 0, a.V);  // (g has the same alignment)
+  if (a.weights && a.weights[row] == 0.f) {
+    zero_span<NT>(g, sp);
+    if (tid == 0) {
+      if (a.logp) a.logp[row] = 0.f;
+      if (a.kl) a.kl[row] = 0.f;
+      a.terms[row] = 0.0;
+    }
+    return;
+  }
+  const int y = clamp_id(a.tokens[row], a.V);
+  const float xy = x[y];
+  const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
+  f32x4 h[H];
+#pragma unroll
+  for (int i = 0; i < H; ++i) h[i] = x4[i * NT + tid];
+  if (L > 0) {
+    const int wave = wave_id();
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+      __builtin_amdgcn_global_load_lds((held_gptr_t)(x4 + (H + l) * NT + tid),
+                                       (held_lptr_t)(smem + (l * WAVES + wave) * 1024), 16, 0, 0);
+  }
+  SoftPart p = kNone;
+  float R = ref_of(p.m, a.c);
+#pragma unroll
+  for (int i = 0; i < H; i += 4) {
+    float f[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = h[i + (e >> 2)][e & 3];
+    soft_add<16, false>(p, R, f, a.c);
+  }
+  if (L > 0) {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's groups are in LDS, which only it reads
+    __builtin_amdgcn_sched_barrier(0);
+    for (int l = 0; l < L; ++l) {
+      const f32x4 v = lds[l * NT + tid];
+      const float f[4] = {v[0], v[1], v[2], v[3]};
+      soft_add<4, false>(p, R, f, a.c);
+    }
+  }
+  for (int q = (H + L) * NT + tid; q < sp.n4; q += NT) {
+    const f32x4 v = x4[q];
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    soft_add<4, false>(p, R, f, a.c);
+  }
+  if (tid < sp.outer) {
+    const float f[1] = {x[sp.outer_at(tid)]};
+    soft_add<1, false>(p, R, f, a.c);
+  }
+  p = block_soft<WAVES>(p, red, a.c);
+  if (far_out(p.m, a.c)) p = far_out_part<WAVES>(x, 0, a.V, p.m, a.c, red);
+  if (tid == 0) {
+    const RowTerms r = row_terms(a, row, xy, p);
+    if (a.logp) a.logp[row] = r.logp;
+    if (a.kl) a.kl[row] = r.kl;
+    a.terms[row] = r.term;
+    sh = grad_row(r, p, a.c);
+  }
+  __syncthreads();
+  const GradRow gr = sh;
+  if (gr.k == 0.f && gr.coef == 0.f) {
+    zero_span<NT>(g, sp);
+    return;
+  }
+  f32x4* g4 = reinterpret_cast<f32x4*>(g + sp.a4);
+#pragma unroll
+  for (int i = 0; i < H; ++i) g4[i * NT + tid] = grad_of4(h[i], gr, a.c);
+  for (int l = 0; l < L; ++l) g4[(H + l) * NT + tid] = grad_of4(lds[l * NT + tid], gr, a.c);
+  for (int q = (H + L) * NT + tid; q < sp.n4; q += NT) g4[q] = grad_of4(x4[q], gr, a.c);
+  if (tid < sp.outer) {
+    const int v = sp.outer_at(tid);
+    g[v] = grad_of(x[v], gr, a.c);
+  }
+  if (tid == sp.owner(y, NT)) g[y] = grad_of(xy, gr, a.c) + gr.coef;
+}
+
+template <int H, int L>
+static hipError_t launch_held(const PolicyDev& d, hipStream_t s) {
+  auto kern = policy_held_kernel<H, L>;
+  constexpr int lds = L * kHeldThreads * 16;
+  if (lds > 0) {
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)d.held), dim3(kHeldThreads), lds, s, d);
+  return hipGetLastError();
+}
+
+// Whole groups of 4 logits that every thread of a held row has at least.
+static int held_groups(int V) { return V < 8 ? 0 : ((V - 6) / 4) / kHeldThreads; }
+
+static Base2 base2_factor(double temperature) {
+  const double c = 1.4426950408889634 / temperature;
+  float hi = (float)c;
+  if ((double)hi >= c) hi = nextafterf(hi, 0.f);
   return Base2{hi, (float)(c - (double)hi)};
 }
 
 template <bool ENT>
-static void launch_stats(int rows, int V, int S, Base2 c, const float* logits, const int32_t* tokens,
-                         const float* weights, float4* stats, float* xy, hipStream_t s) {
-  hipLaunchKernelGGL((policy_stats_kernel<ENT>), dim3((unsigned)rows, (unsigned)S), dim3(kPolThreads), 0, s, V, S, c,
-                     logits, tokens, weights, stats, xy);
+static void launch_stats(int row0, int rows, int V, int S, Base2 c, const float* logits, const int32_t* tokens,
+                         const float* weights, SoftPart* stats, float* xy, hipStream_t s) {
+  hipLaunchKernelGGL((policy_stats_kernel<ENT>), dim3((unsigned)(rows - row0), (unsigned)S), dim3(kPolThreads), 0, s,
+                     row0, V, S, c, logits, tokens, weights, stats, xy);
 }
 
 hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
-                                 float temperature, float* logp, float* entropy, const PolicyPlan& plan,
+                                 double temperature, float* logp, float* entropy, const PolicyPlan& plan,
                                  void* workspace, hipStream_t s) {
   if (B <= 0) return hipSuccess;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  float4* stats = reinterpret_cast<float4*>(ws + plan.stats);
+  SoftPart* stats = reinterpret_cast<SoftPart*>(ws + plan.stats);
   float* xy = reinterpret_cast<float*>(ws + plan.xy);
   const int rows = B * K;
   const Base2 c = base2_factor(temperature);
   if (entropy)
-    launch_stats<true>(rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
+    launch_stats<true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
   else
-    launch_stats<false>(rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
+    launch_stats<false>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
   hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((rows + kPolThreads - 1) / kPolThreads)), dim3(kPolThreads),
-                     0, s, rows, plan.S, c, 1.0 / (double)temperature, stats, xy, weights, logp, entropy);
+                     0, s, rows, plan.S, c, 1.0 / temperature, stats, xy, weights, logp, entropy);
   return hipGetLastError();
 }
 
-hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void* workspace, hipStream_t s) {
+hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void* workspace, int num_cu,
+                              hipStream_t s) {
   if (a.B <= 0) return hipSuccess;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  float4* stats = reinterpret_cast<float4*>(ws + plan.stats);
+  SoftPart* stats = reinterpret_cast<SoftPart*>(ws + plan.stats);
   float* xy = reinterpret_cast<float*>(ws + plan.xy);
   const int rows = a.B * a.K;
-  const PolicyDev d{rows,
-                    a.V,
-                    plan.S,
-                    base2_factor(a.temperature),
-                    1.0 / (double)a.temperature,
-                    1.0 - (double)a.clip_low,
-                    1.0 + (double)a.clip_high,
-                    (double)a.kl_coef,
-                    a.logits,
-                    a.old_logp,
-                    a.ref_logp,
-                    a.advantages,
-                    a.weights,
-                    a.tokens,
-                    stats,
-                    xy,
-                    a.loss,
-                    a.logp,
-                    a.kl,
-                    a.grad};
-  launch_stats<false>(rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, s);
-  const unsigned grid = a.grad ? 1u + (unsigned)rows * (unsigned)plan.S : 1u;
+  PolicyDev d{rows,
+              0,
+              a.V,
+              plan.S,
+              base2_factor(a.temperature),
+              1.0 / a.temperature,
+              1.0 - a.clip_low,
+              1.0 + a.clip_high,
+              a.kl_coef,
+              a.logits,
+              a.old_logp,
+              a.ref_logp,
+              a.advantages,
+              a.weights,
+              a.tokens,
+              stats,
+              xy,
+              reinterpret_cast<double*>(ws + plan.terms),
+              a.loss,
+              a.logp,
+              a.kl,
+              a.grad};
+  const int groups = held_groups(a.V);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad)) & 15u) == 0;
+  if (a.grad && aligned && groups >= 8) {
+    d.held = rows / num_cu * num_cu;
+    hipError_t e = hipSuccess;
+    if (d.held) {
+      e = groups >= 63   ? launch_held<44, 19>(d, s)
+          : groups >= 44 ? launch_held<44, 0>(d, s)
+          : groups >= 36 ? launch_held<36, 0>(d, s)
+          : groups >= 24 ? launch_held<24, 0>(d, s)
+          : groups >= 16 ? launch_held<16, 0>(d, s)
+                         : launch_held<8, 0>(d, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (d.held < rows) launch_stats<false>(d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, s);
+  const unsigned grid = a.grad ? 1u + (unsigned)(rows - d.held) * (unsigned)plan.S : 1u;
   hipLaunchKernelGGL(policy_grad_kernel, dim3(grid), dim3(kPolThreads), 0, s, d);
   return hipGetLastError();
 }

@@ -19,14 +19,17 @@ struct PolicyArgs {
   const float* logits;      // [B K][V]
   const int32_t* tokens;    // [B K], as are the following
   const float *old_logp, *ref_logp, *advantages, *weights;
-  float temperature, clip_low, clip_high, kl_coef;
+  double temperature, clip_low, clip_high, kl_coef;
   float *loss, *logp, *kl, *grad;  // [1], [B K], [B K], [B K][V]; all but loss may be null
 };
 
+constexpr size_t kPolicyPart = 24;  // float, double, double
+
 struct PolicyPlan {
   int S;         // vocabulary slices per row
-  size_t stats;  // byte offset of the [B K][S] float4 partials (max, sum, sum of e t)
+  size_t stats;  // byte offset of the [B K][S] partials (max, sum, sum of e t: kPolicyPart bytes)
   size_t xy;     // byte offset of the [B K] float logits of the tokens
+  size_t terms;  // byte offset of the [B K] double loss terms of rows held on chip
   size_t total;  // workspace bytes
 };
 
@@ -42,8 +45,9 @@ inline PolicyPlan policy_plan(int B, int K, int V) {
   S = S < 1 ? 1 : S > smax ? smax : S;
   p.S = (int)S;
   p.stats = 0;
-  p.xy = align256((size_t)rows * p.S * 16);
-  p.total = align256(p.xy + (size_t)rows * 4);
+  p.xy = align256((size_t)rows * p.S * kPolicyPart);
+  p.terms = align256(p.xy + (size_t)rows * 4);
+  p.total = align256(p.terms + (size_t)rows * 8);
   return p;
 }
 

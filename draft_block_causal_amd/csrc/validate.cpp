@@ -263,8 +263,10 @@ int check_base_i8_args(int32_t batch, int32_t block, int32_t d, int32_t vocab, c
   return DOMINO_OK;
 }
 
-static bool bad_temperature(float t) {
-  return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(1.4426950408889634f / t);
+// (the kernels hold log2(e) / T in float32)
+static bool bad_temperature(double t) {
+  return !(t > 0.0) || !std::isfinite(t) || !std::isfinite((float)(1.4426950408889634 / t)) ||
+         (float)(1.4426950408889634 / t) < 1e-20f;
 }
 
 static bool policy_shape(int32_t batch, int32_t block, int32_t vocab) {
@@ -296,7 +298,7 @@ static int check_policy_workspace(int32_t batch, int32_t block, int32_t vocab, c
 }
 
 int check_logprobs_args(int32_t batch, int32_t block, int32_t vocab, const float* logits, const int32_t* tokens,
-                        const float* weights, float temperature, const float* logp, const float* entropy,
+                        const float* weights, double temperature, const float* logp, const float* entropy,
                         const void* workspace, size_t workspace_bytes) {
   if (!policy_shape(batch, block, vocab)) return DOMINO_ERR_SHAPE;
   if ((long)batch * block > kMaxPolicyRows) return DOMINO_ERR_UNSUPPORTED;
@@ -317,12 +319,12 @@ int check_policy_args(const PolicyArgs& a, const void* workspace, size_t workspa
   if (!policy_shape(a.B, a.K, a.V)) return DOMINO_ERR_SHAPE;
   if ((long)a.B * a.K > kMaxPolicyRows) return DOMINO_ERR_UNSUPPORTED;
   if (bad_temperature(a.temperature)) return DOMINO_ERR_ARG;
-  if (!std::isfinite(a.clip_low) || a.clip_low < 0.f || a.clip_low > 1.f) return DOMINO_ERR_ARG;
-  if (!std::isfinite(a.clip_high) || a.clip_high < 0.f) return DOMINO_ERR_ARG;
-  if (!std::isfinite(a.kl_coef) || a.kl_coef < 0.f) return DOMINO_ERR_ARG;
+  if (!std::isfinite(a.clip_low) || a.clip_low < 0.0 || a.clip_low > 1.0) return DOMINO_ERR_ARG;
+  if (!std::isfinite(a.clip_high) || a.clip_high < 0.0) return DOMINO_ERR_ARG;
+  if (!std::isfinite(a.kl_coef) || a.kl_coef < 0.0) return DOMINO_ERR_ARG;
   if (a.B == 0) return DOMINO_OK;
   if (!a.logits || !a.tokens || !a.old_logp || !a.advantages || !a.loss) return DOMINO_ERR_NULL;
-  if (!a.ref_logp && a.kl_coef != 0.f) return DOMINO_ERR_NULL;
+  if (!a.ref_logp && a.kl_coef != 0.0) return DOMINO_ERR_NULL;
   for (const void* q : {(const void*)a.logits, (const void*)a.tokens, (const void*)a.old_logp,
                         (const void*)a.ref_logp, (const void*)a.advantages, (const void*)a.weights,
                         (const void*)a.loss, (const void*)a.logp, (const void*)a.kl, (const void*)a.grad})

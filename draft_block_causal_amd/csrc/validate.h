@@ -67,7 +67,7 @@ int check_base_i8_args(int32_t batch, int32_t block, int32_t d, int32_t vocab, c
                        const float* hidden_scale, const int8_t* lm_head_q, const float* lm_head_scale,
                        const float* base_logits);
 int check_logprobs_args(int32_t batch, int32_t block, int32_t vocab, const float* logits, const int32_t* tokens,
-                        const float* weights, float temperature, const float* logp, const float* entropy,
+                        const float* weights, double temperature, const float* logp, const float* entropy,
                         const void* workspace, size_t workspace_bytes);
 int check_policy_args(const PolicyArgs& a, const void* workspace, size_t workspace_bytes);
 

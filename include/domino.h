@@ -439,18 +439,18 @@ int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab
  * logits      [batch, block, vocab] float32 (4-byte aligned)
  * tokens      [batch, block] int32; ids outside [0, vocab) are clamped
  * weights     [batch, block] float32, or NULL: every position counts
- * temperature T > 0 with T and log2(e) / T finite (else DOMINO_ERR_ARG)
+ * temperature T > 0, 2e-38 < T < 1e20 (else DOMINO_ERR_ARG)
  * logp, entropy [batch, block] float32 (outputs); they overlap no input and
  *             not each other (else DOMINO_ERR_ARG)
  * workspace   device scratch of at least domino_token_logprobs_workspace_size()
  *             bytes, 256-byte aligned; its contents are overwritten.
  * batch in 0 ... 2^20 (0 is a no-op), block in 1 ... 1024, vocab in 1 ...
- * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).  Arithmetic: exponentials and their sums in float32, merged over
- * vocabulary slices in a fixed order (repeated calls give the same bits); the
+ * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).  Arithmetic: exponentials in float32, summed in float64 over
+ * groups of 16 in a fixed order (repeated calls give the same bits); the
  * logarithm and the differences in float64.
  */
 int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
-                          const float *weights, float temperature, float *logp, float *entropy, void *workspace,
+                          const float *weights, double temperature, float *logp, float *entropy, void *workspace,
                           size_t workspace_bytes, void *stream);
 
 /* Workspace bytes domino_token_logprobs needs (0 for sizes out of range). */
@@ -503,7 +503,7 @@ size_t domino_token_logprobs_workspace_size(int32_t batch, int32_t block, int32_
  */
 int domino_policy_loss(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
                        const float *old_logp, const float *ref_logp, const float *advantages, const float *weights,
-                       float temperature, float clip_low, float clip_high, float kl_coef, float *loss, float *logp,
+                       double temperature, double clip_low, double clip_high, double kl_coef, float *loss, float *logp,
                        float *kl, float *grad, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Workspace bytes domino_policy_loss needs (0 for sizes out of range). */

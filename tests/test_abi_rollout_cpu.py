@@ -65,7 +65,7 @@ def test_token_logprobs_refusals(lib):
     assert _logp(lib, B=-1) == _logp(lib, B=(1 << 20) + 1) == _logp(lib, K=0) == _logp(lib, K=1025) == E_SHAPE
     assert _logp(lib, V=0) == _logp(lib, V=1 << 24) == E_SHAPE
     assert _logp(lib, B=1 << 20, K=5, nb=1 << 40) == E_UNSUP
-    for T in (0.0, -1.0, NAN, INF, 1e-39):
+    for T in (0.0, -1.0, NAN, INF, 1e-39, 1e21):
         assert _logp(lib, T=T) == E_ARG
     assert _logp(lib, logits=None) == _logp(lib, tokens=None) == _logp(lib, logp=None) == E_NULL
     assert _logp(lib, logits=0x100002) == _logp(lib, w=0x50001) == _logp(lib, ent=0x60002) == E_ALIGN
