@@ -79,11 +79,18 @@ __device__ __forceinline__ SoftPart soft_merge(SoftPart a, SoftPart b, Base2 c) 
   return SoftPart{m, a.s + b.s, a.u + b.u};
 }
 
-__device__ __forceinline__ SoftPart wave_soft(SoftPart p, Base2 c) {
+// Over groups of WIDTH lanes: the maximum first, then every lane's sums brought
+// to it once and added up.
+template <int WIDTH>
+__device__ __forceinline__ SoftPart lanes_soft(SoftPart p, Base2 c) {
+  float m = p.m;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const SoftPart q{__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.u, o)};
-    p = soft_merge(p, q, c);
+  for (int o = WIDTH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  p = soft_to(p, m, c);
+#pragma unroll
+  for (int o = WIDTH / 2; o > 0; o >>= 1) {
+    p.s += __shfl_xor(p.s, o);
+    p.u += __shfl_xor(p.u, o);
   }
   return p;
 }
@@ -151,7 +158,7 @@ struct Span {
 // 0 at least.  red: one entry per wave.
 template <int WAVES>
 __device__ __forceinline__ SoftPart block_soft(SoftPart p, SoftPart* red, Base2 c) {
-  p = wave_soft(p, c);
+  p = lanes_soft<64>(p, c);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = p;
   __syncthreads();
   p = red[0];
@@ -187,7 +194,7 @@ __device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 
   return p;
 }
 
-template <bool ENT>
+template <bool ENT, bool ONCE>
 __global__ void __launch_bounds__(kPolThreads)
     policy_stats_kernel(int row0, int V, int S, Base2 c, const float* __restrict__ logits,
                         const int32_t* __restrict__ tokens, const float* __restrict__ weights,
@@ -206,7 +213,8 @@ __global__ void __launch_bounds__(kPolThreads)
   for (; q + 3 * kPolThreads < sp.n4; q += 4 * kPolThreads) {
     f32x4 f4[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f4[i] = x4[q + i * kPolThreads];
+    for (int i = 0; i < 4; ++i)
+      f4[i] = ONCE ? __builtin_nontemporal_load(x4 + q + i * kPolThreads) : x4[q + i * kPolThreads];
     float f[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) f[e] = f4[e >> 2][e & 3];
@@ -230,14 +238,22 @@ __global__ void __launch_bounds__(kPolThreads)
   }
 }
 
-// Slices in order.  (A far-out slice below a maximum that is not adds nothing.)
-__device__ __forceinline__ SoftPart slice_merge(SoftPart a, SoftPart b, Base2 c) {
-  const float m = fmaxf(a.m, b.m);
-  if (!far_out(m, c)) return soft_merge(a, b, c);
-  const float ta = a.m == -INFINITY ? -INFINITY : (a.m - m) * c.hi, tb = b.m == -INFINITY ? -INFINITY : (b.m - m) * c.hi;
-  const float ea = exp2_hw(ta), eb = exp2_hw(tb);
-  return SoftPart{m, ea * a.s + eb * b.s,
-                  ea * (a.u + fmaxf(ta, -200.f) * a.s) + eb * (b.u + fmaxf(tb, -200.f) * b.s)};
+// The part of a row from its S <= 32 slices' parts, one a lane of a group of 32
+// (kNone in the other lanes); the result in every lane of the group.  (A
+// far-out slice below a maximum that is not adds nothing.)
+__device__ __forceinline__ SoftPart slices_soft(SoftPart p, Base2 c) {
+  float m = p.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if (!far_out(m, c)) return lanes_soft<32>(p, c);
+  const float t = p.m == -INFINITY ? -INFINITY : (p.m - m) * c.hi, e = exp2_hw(t);
+  p = SoftPart{m, e * p.s, e * (p.u + fmaxf(t, -200.f) * p.s)};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    p.s += __shfl_xor(p.s, o);
+    p.u += __shfl_xor(p.u, o);
+  }
+  return p;
 }
 
 // ln of the row's sum with the part of logp before it: logp = shift(x_y) - ln s.
@@ -247,16 +263,16 @@ __device__ __forceinline__ double shift_of(float xy, const SoftPart& p, Base2 c,
 }
 
 __device__ __forceinline__ SoftPart row_part(const SoftPart* stats, int row, int S, Base2 c) {
-  SoftPart p = stats[(size_t)row * S];
-  for (int q = 1; q < S; ++q) p = slice_merge(p, stats[(size_t)row * S + q], c);
-  return p;
+  const int q = threadIdx.x & 31;
+  return slices_soft(q < S ? stats[(size_t)row * S + q] : kNone, c);
 }
 
+// 32 lanes a row
 __global__ void __launch_bounds__(kPolThreads)
     logprobs_rows_kernel(int rows, int S, Base2 c, double inv_t, const SoftPart* __restrict__ stats,
                          const float* __restrict__ xy, const float* __restrict__ weights, float* __restrict__ logp,
                          float* __restrict__ entropy) {
-  const int row = blockIdx.x * kPolThreads + threadIdx.x;
+  const int row = blockIdx.x * (kPolThreads / 32) + (threadIdx.x >> 5);
   if (row >= rows) return;
   float lp = 0.f, h = 0.f;
   if (!(weights && weights[row] == 0.f)) {
@@ -269,8 +285,10 @@ __global__ void __launch_bounds__(kPolThreads)
       h = (float)(ln_s - 0.6931471805599453 * (p.u / p.s));
     }
   }
-  logp[row] = lp;
-  if (entropy) entropy[row] = h;
+  if ((threadIdx.x & 31) == 0) {
+    logp[row] = lp;
+    if (entropy) entropy[row] = h;
+  }
 }
 
 struct PolicyDev {
@@ -320,29 +338,30 @@ __device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, float
 }
 
 // Workgroup 0 of policy_grad_kernel: logp and kl of the rows that are not held,
-// and the loss, each thread adding rows t, t + 256, ... in order and a fixed tree
-// over the threads' sums.
+// and the loss: 32 lanes a row for the terms, the first of which adds up rows
+// r, r + 8, ... in order; the held rows' terms are dealt out to all threads; then
+// a fixed tree over the threads' sums.
 __device__ void policy_rows(const PolicyDev& a) {
-  __shared__ double part[kPolThreads];
+  __shared__ double part[kPolWaves];
   double acc = 0.0;
-  for (int row = threadIdx.x; row < a.rows; row += kPolThreads) {
-    if (row < a.held) {
-      acc += a.terms[row];
-      continue;
-    }
+  for (int row = threadIdx.x; row < a.held; row += kPolThreads) acc += a.terms[row];
+  for (int row = a.held + (threadIdx.x >> 5); row < a.rows; row += kPolThreads / 32) {
     RowTerms r{0.f, 0.f, 0.0, 0.0};
     if (!(a.weights && a.weights[row] == 0.f)) r = row_terms(a, row, a.xy[row], row_part(a.stats, row, a.S, a.c));
-    if (a.logp) a.logp[row] = r.logp;
-    if (a.kl) a.kl[row] = r.kl;
-    acc += r.term;
+    if ((threadIdx.x & 31) == 0) {
+      if (a.logp) a.logp[row] = r.logp;
+      if (a.kl) a.kl[row] = r.kl;
+      acc += r.term;
+    }
   }
-  part[threadIdx.x] = acc;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
   __syncthreads();
-  for (int h = kPolThreads / 2; h > 0; h >>= 1) {
-    if ((int)threadIdx.x < h) part[threadIdx.x] += part[threadIdx.x + h];
-    __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kPolWaves; ++w) acc += part[w];
+    a.loss[0] = (float)acc;
   }
-  if (threadIdx.x == 0) a.loss[0] = (float)part[0];
 }
 
 // What a row's gradient is made of: grad = k 2^t (+ coef at the token).
@@ -391,17 +410,10 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
     return;
   }
   const float xy = a.xy[row];
-  if (threadIdx.x < 64) {
-    // each lane takes one slice (S <= 32)
-    const int q = threadIdx.x;
-    SoftPart p = kNone;
-    if (q < a.S) p = a.stats[(size_t)row * a.S + q];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const SoftPart r{__shfl_xor(p.m, o), __shfl_xor(p.s, o), __shfl_xor(p.u, o)};
-      p = slice_merge(p, r, a.c);
-    }
-    if (q == 0) sh = grad_row(row_terms(a, row, xy, p), p, a.c);
+  if (threadIdx.x < 32) {
+    const SoftPart p = row_part(a.stats, row, a.S, a.c);
+    const RowTerms r = row_terms(a, row, xy, p);
+    if (threadIdx.x == 0) sh = grad_row(r, p, a.c);
   }
   __syncthreads();
   const GradRow gr = sh;
@@ -430,17 +442,25 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
 }
 
 // ---------------------------------------------------------------------------
-// Held rows: 512 threads, H groups of 4 logits a thread in registers, L more in
-// LDS (filled by loads that bypass the registers), the rest read twice.  All
-// loads of the held groups are issued at once, so a compute unit has up to 580
-// KB in flight, and the row's terms are added up as they come in.
+// Held rows: 512 threads; a layer is 512 groups of 4 logits, one a thread.  H
+// layers stay in registers, up to kHeldLds more in LDS (filled by loads that
+// bypass the registers), and up to RM (the rest, the last one ragged) are read
+// twice: before the registers fill up, and again into those freed by the first
+// layers' gradients, so that no load is waited for alone.  What is beyond comes
+// in a plain loop.  All other loads of a row are in flight at once, up to 500 KB
+// a compute unit, and the row's terms are added up as they come in.
+// Non-temporal both ways: nothing is read again from a cache but the RM layers
+// (32 blocks of the Qwen3 vocabulary: 164 -> 137 us with RM layers read in a
+// loop each time, HELDUS in this form).
 // ---------------------------------------------------------------------------
 constexpr int kHeldThreads = 512;
+constexpr int kHeldLds = 19;  // 152 KB
 typedef __attribute__((address_space(1))) const void* held_gptr_t;
 typedef __attribute__((address_space(3))) void* held_lptr_t;
 
-template <int H, int L>
-__global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a) {
+template <int H, int RM>
+__global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a, int L) {
+  static_assert(H % 4 == 0 && RM % 4 == 0 && H > RM, "layers go in fours");
   constexpr int NT = kHeldThreads, WAVES = NT / 64;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   f32x4* lds = reinterpret_cast<f32x4*>(smem);  // [L][NT]
@@ -462,35 +482,63 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a) 
   const int y = clamp_id(a.tokens[row], a.V);
   const float xy = x[y];
   const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
-  f32x4 h[H];
-#pragma unroll
-  for (int i = 0; i < H; ++i) h[i] = x4[i * NT + tid];
-  if (L > 0) {
-    const int wave = wave_id();
-#pragma unroll
-    for (int l = 0; l < L; ++l)
-      __builtin_amdgcn_global_load_lds((held_gptr_t)(x4 + (H + l) * NT + tid),
-                                       (held_lptr_t)(smem + (l * WAVES + wave) * 1024), 16, 0, 0);
-  }
+  const int rest = (H + L) * NT;  // the first group that is not held
   SoftPart p = kNone;
   float R = ref_of(p.m, a.c);
-#pragma unroll
-  for (int i = 0; i < H; i += 4) {
+  auto add4 = [&](const f32x4* v) {
     float f[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = h[i + (e >> 2)][e & 3];
+    for (int e = 0; e < 16; ++e) f[e] = v[e >> 2][e & 3];
     soft_add<16, false>(p, R, f, a.c);
+  };
+  auto load_rest = [&](f32x4 (&r)[RM]) {
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+      if (rest + i * NT < sp.n4) r[i] = x4[min(rest + i * NT + tid, sp.n4 - 1)];
+  };
+  if (L > 0) {
+    const int wave = wave_id();
+    for (int l = 0; l < L; ++l)
+      __builtin_amdgcn_global_load_lds((held_gptr_t)(x4 + (H + l) * NT + tid),
+                                       (held_lptr_t)(smem + (l * WAVES + wave) * 1024), 16, 0, kLoadNonTemporal);
   }
+  f32x4 h[H];
+  {
+    f32x4 r[RM];
+    load_rest(r);
+#pragma unroll
+    for (int i = 0; i < H - RM; ++i) h[i] = __builtin_nontemporal_load(x4 + i * NT + tid);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+      if (rest + i * NT < sp.n4) {
+        const bool in = rest + i * NT + tid < sp.n4;
+        const float f[4] = {in ? r[i][0] : -INFINITY, in ? r[i][1] : -INFINITY, in ? r[i][2] : -INFINITY,
+                            in ? r[i][3] : -INFINITY};
+        soft_add<4, false>(p, R, f, a.c);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = H - RM; i < H; ++i) h[i] = __builtin_nontemporal_load(x4 + i * NT + tid);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < H; i += 4) add4(h + i);
   if (L > 0) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's groups are in LDS, which only it reads
     __builtin_amdgcn_sched_barrier(0);
-    for (int l = 0; l < L; ++l) {
+    int l = 0;
+    for (; l + 4 <= L; l += 4) {
+      const f32x4 v[4] = {lds[l * NT + tid], lds[(l + 1) * NT + tid], lds[(l + 2) * NT + tid], lds[(l + 3) * NT + tid]};
+      add4(v);
+    }
+    for (; l < L; ++l) {
       const f32x4 v = lds[l * NT + tid];
       const float f[4] = {v[0], v[1], v[2], v[3]};
       soft_add<4, false>(p, R, f, a.c);
     }
   }
-  for (int q = (H + L) * NT + tid; q < sp.n4; q += NT) {
+  for (int q = rest + RM * NT + tid; q < sp.n4; q += NT) {
     const f32x4 v = x4[q];
     const float f[4] = {v[0], v[1], v[2], v[3]};
     soft_add<4, false>(p, R, f, a.c);
@@ -501,12 +549,14 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a) 
   }
   p = block_soft<WAVES>(p, red, a.c);
   if (far_out(p.m, a.c)) p = far_out_part<WAVES>(x, 0, a.V, p.m, a.c, red);
-  if (tid == 0) {
+  if (tid < 64) {
     const RowTerms r = row_terms(a, row, xy, p);
-    if (a.logp) a.logp[row] = r.logp;
-    if (a.kl) a.kl[row] = r.kl;
-    a.terms[row] = r.term;
-    sh = grad_row(r, p, a.c);
+    if (tid == 0) {
+      if (a.logp) a.logp[row] = r.logp;
+      if (a.kl) a.kl[row] = r.kl;
+      a.terms[row] = r.term;
+      sh = grad_row(r, p, a.c);
+    }
   }
   __syncthreads();
   const GradRow gr = sh;
@@ -515,10 +565,23 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a) 
     return;
   }
   f32x4* g4 = reinterpret_cast<f32x4*>(g + sp.a4);
+  auto put = [&](int q, f32x4 v) { __builtin_nontemporal_store(grad_of4(v, gr, a.c), g4 + q); };
 #pragma unroll
-  for (int i = 0; i < H; ++i) g4[i * NT + tid] = grad_of4(h[i], gr, a.c);
-  for (int l = 0; l < L; ++l) g4[(H + l) * NT + tid] = grad_of4(lds[l * NT + tid], gr, a.c);
-  for (int q = (H + L) * NT + tid; q < sp.n4; q += NT) g4[q] = grad_of4(x4[q], gr, a.c);
+  for (int i = 0; i < RM; ++i) put(i * NT + tid, h[i]);
+  __builtin_amdgcn_sched_barrier(0);
+  {
+    f32x4 r[RM];
+    load_rest(r);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = RM; i < H; ++i) put(i * NT + tid, h[i]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+      if (rest + i * NT + tid < sp.n4) put(rest + i * NT + tid, r[i]);
+  }
+  for (int l = 0; l < L; ++l) put((H + l) * NT + tid, lds[l * NT + tid]);
+  for (int q = rest + RM * NT + tid; q < sp.n4; q += NT) put(q, x4[q]);
   if (tid < sp.outer) {
     const int v = sp.outer_at(tid);
     g[v] = grad_of(x[v], gr, a.c);
@@ -526,21 +589,20 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a) 
   if (tid == sp.owner(y, NT)) g[y] = grad_of(xy, gr, a.c) + gr.coef;
 }
 
-template <int H, int L>
-static hipError_t launch_held(const PolicyDev& d, hipStream_t s) {
-  auto kern = policy_held_kernel<H, L>;
-  constexpr int lds = L * kHeldThreads * 16;
-  if (lds > 0) {
-    const hipError_t e =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+template <int H, int RM>
+static hipError_t launch_held(const PolicyDev& d, int L, hipStream_t s) {
+  auto kern = policy_held_kernel<H, RM>;
+  if (L > 0) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kHeldLds * kHeldThreads * 16);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)d.held), dim3(kHeldThreads), lds, s, d);
+  hipLaunchKernelGGL(kern, dim3((unsigned)d.held), dim3(kHeldThreads), L * kHeldThreads * 16, s, d, L);
   return hipGetLastError();
 }
 
-// Whole groups of 4 logits that every thread of a held row has at least.
-static int held_groups(int V) { return V < 8 ? 0 : ((V - 6) / 4) / kHeldThreads; }
+// Whole layers that every held row has at least.
+static int held_layers(int V) { return V < 8 ? 0 : ((V - 6) / 4) / kHeldThreads; }
 
 static Base2 base2_factor(double temperature) {
   const double c = 1.4426950408889634 / temperature;
@@ -549,10 +611,11 @@ static Base2 base2_factor(double temperature) {
   return Base2{hi, (float)(c - (double)hi)};
 }
 
-template <bool ENT>
+// ONCE: the logits are not read again (non-temporal loads)
+template <bool ENT, bool ONCE>
 static void launch_stats(int row0, int rows, int V, int S, Base2 c, const float* logits, const int32_t* tokens,
                          const float* weights, SoftPart* stats, float* xy, hipStream_t s) {
-  hipLaunchKernelGGL((policy_stats_kernel<ENT>), dim3((unsigned)(rows - row0), (unsigned)S), dim3(kPolThreads), 0, s,
+  hipLaunchKernelGGL((policy_stats_kernel<ENT, ONCE>), dim3((unsigned)(rows - row0), (unsigned)S), dim3(kPolThreads), 0, s,
                      row0, V, S, c, logits, tokens, weights, stats, xy);
 }
 
@@ -566,11 +629,11 @@ hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const
   const int rows = B * K;
   const Base2 c = base2_factor(temperature);
   if (entropy)
-    launch_stats<true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
+    launch_stats<true, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
   else
-    launch_stats<false>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
-  hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((rows + kPolThreads - 1) / kPolThreads)), dim3(kPolThreads),
-                     0, s, rows, plan.S, c, 1.0 / temperature, stats, xy, weights, logp, entropy);
+    launch_stats<false, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
+  hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((rows + kPolThreads / 32 - 1) / (kPolThreads / 32))),
+                     dim3(kPolThreads), 0, s, rows, plan.S, c, 1.0 / temperature, stats, xy, weights, logp, entropy);
   return hipGetLastError();
 }
 
@@ -603,22 +666,20 @@ hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void*
               a.logp,
               a.kl,
               a.grad};
-  const int groups = held_groups(a.V);
+  const int layers = held_layers(a.V);
   const bool aligned = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad)) & 15u) == 0;
-  if (a.grad && aligned && groups >= 8) {
+  if (a.grad && aligned && layers >= 8) {
     d.held = rows / num_cu * num_cu;
-    hipError_t e = hipSuccess;
     if (d.held) {
-      e = groups >= 63   ? launch_held<44, 19>(d, s)
-          : groups >= 44 ? launch_held<44, 0>(d, s)
-          : groups >= 36 ? launch_held<36, 0>(d, s)
-          : groups >= 24 ? launch_held<24, 0>(d, s)
-          : groups >= 16 ? launch_held<16, 0>(d, s)
-                         : launch_held<8, 0>(d, s);
+      const hipError_t e = layers >= 48   ? launch_held<48, 8>(d, std::min(layers - 48, kHeldLds), s)
+                           : layers >= 36 ? launch_held<36, 12>(d, 0, s)
+                           : layers >= 24 ? launch_held<24, 12>(d, 0, s)
+                           : layers >= 16 ? launch_held<16, 8>(d, 0, s)
+                                          : launch_held<8, 4>(d, std::min(layers - 8, 4), s);
       if (e != hipSuccess) return e;
     }
   }
-  if (d.held < rows) launch_stats<false>(d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, s);
+  if (d.held < rows) launch_stats<false, false>(d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, s);
   const unsigned grid = a.grad ? 1u + (unsigned)(rows - d.held) * (unsigned)plan.S : 1u;
   hipLaunchKernelGGL(policy_grad_kernel, dim3(grid), dim3(kPolThreads), 0, s, d);
   return hipGetLastError();

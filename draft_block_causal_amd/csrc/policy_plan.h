@@ -33,13 +33,14 @@ struct PolicyPlan {
   size_t total;  // workspace bytes
 };
 
-// About 2048 workgroups, each slice at least 2048 entries long, and at most 32
+// About 8192 workgroups (positions that are not read leave at once, so that the
+// others must be many to spread evenly), each slice at least 2048 entries long, and at most 32
 // slices per row (one wave merges a row's partials).
 inline PolicyPlan policy_plan(int B, int K, int V) {
   auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PolicyPlan p{};
   const long rows = (long)B * K;
-  long S = (2048 + rows - 1) / rows;
+  long S = (8192 + rows - 1) / rows;
   long smax = V / 2048 > 1 ? V / 2048 : 1;
   smax = smax > 32 ? 32 : smax;
   S = S < 1 ? 1 : S > smax ? smax : S;

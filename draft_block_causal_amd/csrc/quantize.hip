@@ -20,13 +20,19 @@ namespace domino {
 
 constexpr int kQuantWaves = 4;  // rows per workgroup
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u32x4 ldnt16(const unsigned char* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
 template <class T>
 struct Chunk8;  // 8 consecutive values of a row
 
 template <>
 struct Chunk8<Bf16> {
   u32x4 v;
-  __device__ __forceinline__ void load(const unsigned char* row, int chunk) { v = ld16(row + (size_t)chunk * 16); }
+  __device__ __forceinline__ void load(const unsigned char* row, int chunk) { v = ldnt16(row + (size_t)chunk * 16); }
   __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int e) const {
     const uint32_t u = v[e >> 1];
@@ -38,8 +44,8 @@ template <>
 struct Chunk8<F32> {
   u32x4 v[2];
   __device__ __forceinline__ void load(const unsigned char* row, int chunk) {
-    v[0] = ld16(row + (size_t)chunk * 32);
-    v[1] = ld16(row + (size_t)chunk * 32 + 16);
+    v[0] = ldnt16(row + (size_t)chunk * 32);
+    v[1] = ldnt16(row + (size_t)chunk * 32 + 16);
   }
   __device__ __forceinline__ void zero() { v[0] = v[1] = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int e) const { return __uint_as_float(v[e >> 2][e & 3]); }
@@ -87,7 +93,7 @@ __global__ void __launch_bounds__(kQuantWaves * 64)
   const float up = a < 8.673617379884035e-19f ? 18446744073709551616.f : 1.f;  // a < 2^-60
   a *= up;
   const float inv = finite && a > 0.f ? 127.f / a : 0.f;
-  uint2* qr = reinterpret_cast<uint2*>(q + (size_t)row * cols);
+  u32x2* qr = reinterpret_cast<u32x2*>(q + (size_t)row * cols);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     float t[8];
@@ -104,13 +110,13 @@ __global__ void __launch_bounds__(kQuantWaves * 64)
 #pragma unroll
       for (int e = 0; e < 8; ++e) k[e] = round_quotient(c[i].get(e) * up, a, t[e]);
     }
-    uint2 w{0, 0};
+    u32x2 w{0, 0};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w.x |= (uint32_t)(k[e] & 0xFF) << (8 * e);
-      w.y |= (uint32_t)(k[e + 4] & 0xFF) << (8 * e);
+      w[0] |= (uint32_t)(k[e] & 0xFF) << (8 * e);
+      w[1] |= (uint32_t)(k[e + 4] & 0xFF) << (8 * e);
     }
-    if (i * 64 + lane < chunks) qr[i * 64 + lane] = w;
+    if (i * 64 + lane < chunks) __builtin_nontemporal_store(w, qr + i * 64 + lane);
   }
 }
 
