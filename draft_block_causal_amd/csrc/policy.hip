@@ -194,13 +194,27 @@ __device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 
   return p;
 }
 
+// Row of workgroup b of n when a workgroup takes a row: groups of 8 consecutive
+// rows are turned against the 8 XCDs that workgroups go round, each group by
+// another step, so that positions of a block that are often masked (its last
+// ones) do not all fall to the same XCD.
+__device__ __forceinline__ int turned_row(int b, int n) {
+  return (b | 7) < n ? (b & ~7) | ((b + (b >> 3) + (b >> 4)) & 7) : b;
+}
+
+// Workgroup b: slice b % S of row b / S, so that neighbouring slices go to
+// different XCDs (64 blocks cut at their acceptance lengths: with all slices of
+// a row on one XCD 70 us, the XCD of a block's first positions having 1.4 times
+// the average work; POLXCD us).
 template <bool ENT, bool ONCE>
 __global__ void __launch_bounds__(kPolThreads)
-    policy_stats_kernel(int row0, int V, int S, Base2 c, const float* __restrict__ logits,
+    policy_stats_kernel(int row0, int rows, int V, int S, Base2 c, const float* __restrict__ logits,
                         const int32_t* __restrict__ tokens, const float* __restrict__ weights,
-                        SoftPart* __restrict__ stats, float* __restrict__ xy) {
+                        SoftPart* __restrict__ stats, float* __restrict__ xy,
+                        unsigned int* __restrict__ ticket) {
   __shared__ SoftPart red[kPolWaves];
-  const int row = row0 + blockIdx.x, sl = blockIdx.y;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && ticket) *ticket = 0;  // for policy_grad_kernel
+  const int sl = (int)(blockIdx.x % (unsigned)S), row = row0 + turned_row((int)(blockIdx.x / (unsigned)S), rows - row0);
   if (weights && weights[row] == 0.f) return;
   const float* x = logits + (size_t)row * V;
   int v0, v1;
@@ -209,21 +223,40 @@ __global__ void __launch_bounds__(kPolThreads)
   SoftPart p = kNone;
   float R = ref_of(p.m, c);
   const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
-  int q = threadIdx.x;
-  for (; q + 3 * kPolThreads < sp.n4; q += 4 * kPolThreads) {
-    f32x4 f4[4];
+  {
+    // four groups a thread and step, the next step in flight while one is used;
+    // the last step may be ragged
+    constexpr int U = 4, kStep = U * kPolThreads;
+    const int n = (sp.n4 + kStep - 1) / kStep;
+    auto load = [&](f32x4 (&d)[U], int step) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f4[i] = ONCE ? __builtin_nontemporal_load(x4 + q + i * kPolThreads) : x4[q + i * kPolThreads];
-    float f[16];
+      for (int i = 0; i < U; ++i) {
+        const f32x4* at = x4 + min(step * kStep + i * kPolThreads + (int)threadIdx.x, sp.n4 - 1);
+        d[i] = ONCE ? __builtin_nontemporal_load(at) : *at;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto use = [&](f32x4 (&d)[U], int step) {
+      if ((step + 1) * kStep > sp.n4) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = f4[e >> 2][e & 3];
-    soft_add<16, ENT>(p, R, f, c);
-  }
-  for (; q < sp.n4; q += kPolThreads) {
-    const f32x4 f0 = x4[q];
-    const float f[4] = {f0[0], f0[1], f0[2], f0[3]};
-    soft_add<4, ENT>(p, R, f, c);
+        for (int i = 0; i < U; ++i)
+          if (step * kStep + i * kPolThreads + (int)threadIdx.x >= sp.n4)
+            d[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      }
+      float f[4 * U];
+#pragma unroll
+      for (int e = 0; e < 4 * U; ++e) f[e] = d[e >> 2][e & 3];
+      soft_add<4 * U, ENT>(p, R, f, c);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 b0[U], b1[U];
+    if (n > 0) load(b0, 0);
+    for (int i = 0; i < n; i += 2) {
+      if (i + 1 < n) load(b1, i + 1);
+      use(b0, i);
+      if (i + 2 < n) load(b0, i + 2);
+      if (i + 1 < n) use(b1, i + 1);
+    }
   }
   if ((int)threadIdx.x < sp.outer) {
     const float f[1] = {x[sp.outer_at(threadIdx.x)]};
@@ -292,14 +325,18 @@ __global__ void __launch_bounds__(kPolThreads)
 }
 
 struct PolicyDev {
-  int rows, held, V, S;  // rows below `held` are the held kernel's
+  int rows, held, V;  // rows below `held` are the held kernel's
+  int S, G;           // slices of a row's statistics, and of its gradient
   Base2 c;
   double inv_t, lo, hi, beta;  // clip range limits; KL coefficient
   const float *logits, *old_logp, *ref_logp, *advantages, *weights;
   const int32_t* tokens;
   const SoftPart* stats;
   const float* xy;
-  double* terms;  // [held] weighted loss terms
+  double* terms;        // [held] weighted loss terms
+  double* sums;         // [row_wgs] sums of the other rows' terms
+  unsigned int* ticket;  // finished row workgroups (0 at the kernel's start)
+  int row_wgs;
   float *loss, *logp, *kl, *grad;
 };
 
@@ -337,23 +374,48 @@ __device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, float
   return r;
 }
 
-// Workgroup 0 of policy_grad_kernel: logp and kl of the rows that are not held,
-// and the loss: 32 lanes a row for the terms, the first of which adds up rows
-// r, r + 8, ... in order; the held rows' terms are dealt out to all threads; then
-// a fixed tree over the threads' sums.
+// The first `row_wgs` workgroups of policy_grad_kernel: logp, kl and the loss
+// terms of the rows that are not held, 32 lanes a row and kRowsPerWg rows a
+// workgroup, summed in order; the workgroup that finishes last adds up the
+// workgroups' sums and the held rows' terms in a fixed order, so that the order
+// of finishing does not show.
+constexpr int kRowsPerWg = kPolThreads / 32;
+
 __device__ void policy_rows(const PolicyDev& a) {
-  __shared__ double part[kPolWaves];
-  double acc = 0.0;
-  for (int row = threadIdx.x; row < a.held; row += kPolThreads) acc += a.terms[row];
-  for (int row = a.held + (threadIdx.x >> 5); row < a.rows; row += kPolThreads / 32) {
+  __shared__ double part[kRowsPerWg];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
+  const int row = a.held + (int)blockIdx.x * kRowsPerWg + sub;
+  double term = 0.0;
+  if (row < a.rows) {
     RowTerms r{0.f, 0.f, 0.0, 0.0};
     if (!(a.weights && a.weights[row] == 0.f)) r = row_terms(a, row, a.xy[row], row_part(a.stats, row, a.S, a.c));
-    if ((threadIdx.x & 31) == 0) {
+    term = r.term;
+    if (lane == 0) {
       if (a.logp) a.logp[row] = r.logp;
       if (a.kl) a.kl[row] = r.kl;
-      acc += r.term;
     }
   }
+  if (lane == 0) part[sub] = term;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double sum = part[0];
+    for (int q = 1; q < kRowsPerWg; ++q) sum += part[q];
+    last = true;
+    if (a.row_wgs > 1) {
+      __hip_atomic_store(a.sums + blockIdx.x, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             (unsigned)a.row_wgs - 1u;
+    } else {
+      a.sums[0] = sum;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  double acc = 0.0;
+  for (int q = threadIdx.x; q < a.row_wgs; q += kPolThreads)
+    acc += __hip_atomic_load(a.sums + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int q = threadIdx.x; q < a.held; q += kPolThreads) acc += a.terms[q];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = acc;
@@ -393,22 +455,33 @@ __device__ __forceinline__ void zero_span(float* g, const Span& sp) {
 // (x and g may be the same buffer: every entry is read by the thread that
 // writes it, before it does, and the token's logit comes from xy)
 __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
-  if (blockIdx.x == 0) {
+  if ((int)blockIdx.x < a.row_wgs) {
     policy_rows(a);
     return;
   }
   __shared__ GradRow sh;
-  const unsigned b = blockIdx.x - 1;
-  const int row = a.held + (int)(b / (unsigned)a.S), sl = (int)(b % (unsigned)a.S);
+  const unsigned b = blockIdx.x - (unsigned)a.row_wgs;
+  const int row = a.held + (int)(b / (unsigned)a.G), sl = (int)(b % (unsigned)a.G);
   const float* x = a.logits + (size_t)row * a.V;
   float* g = a.grad + (size_t)row * a.V;
   int v0, v1;
-  row_slice(x, a.V, sl, a.S, v0, v1);
+  row_slice(x, a.V, sl, a.G, v0, v1);
   const Span sp(g, v0, v1);
   if (a.weights && a.weights[row] == 0.f) {  // nothing is read
     zero_span<kPolThreads>(g, sp);
     return;
   }
+  const bool alike = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0;
+  // the first groups are on their way while the row's sums are brought together
+  constexpr int U = 4, kStep = U * kPolThreads;
+  f32x4 d[U];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      d[i] = *reinterpret_cast<const f32x4*>(x + sp.a4 + 4 * min(at + i * kPolThreads + (int)threadIdx.x, sp.n4 - 1));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (alike && sp.n4 > 0) load(0);
   const float xy = a.xy[row];
   if (threadIdx.x < 32) {
     const SoftPart p = row_part(a.stats, row, a.S, a.c);
@@ -417,15 +490,19 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
   }
   __syncthreads();
   const GradRow gr = sh;
-  if (gr.k == 0.f && gr.coef == 0.f) {  // nor here
+  if (gr.k == 0.f && gr.coef == 0.f) {  // no gradient here
     zero_span<kPolThreads>(g, sp);
     return;
   }
   const int y = clamp_id(a.tokens[row], a.V);
-  if (((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0) {
-    for (int q = threadIdx.x; q < sp.n4; q += kPolThreads) {
-      const int v = sp.a4 + 4 * q;
-      *reinterpret_cast<f32x4*>(g + v) = grad_of4(*reinterpret_cast<const f32x4*>(x + v), gr, a.c);
+  if (alike) {
+    for (int at = 0; at < sp.n4; at += kStep) {
+      if (at > 0) load(at);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int q = at + i * kPolThreads + (int)threadIdx.x;
+        if (q < sp.n4) *reinterpret_cast<f32x4*>(g + sp.a4 + 4 * q) = grad_of4(d[i], gr, a.c);
+      }
     }
     if ((int)threadIdx.x < sp.outer) {
       const int v = sp.outer_at(threadIdx.x);
@@ -442,7 +519,7 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
 }
 
 // ---------------------------------------------------------------------------
-// Held rows: 512 threads; a layer is 512 groups of 4 logits, one a thread.  H
+// Held rows: NT threads; a layer is NT groups of 4 logits, one a thread.  H
 // layers stay in registers, up to kHeldLds more in LDS (filled by loads that
 // bypass the registers), and up to RM (the rest, the last one ragged) are read
 // twice: before the registers fill up, and again into those freed by the first
@@ -453,20 +530,20 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
 // (32 blocks of the Qwen3 vocabulary: 164 -> 137 us with RM layers read in a
 // loop each time, HELDUS in this form).
 // ---------------------------------------------------------------------------
-constexpr int kHeldThreads = 512;
-constexpr int kHeldLds = 19;  // 152 KB
+constexpr int kHeldMost = 100;  // layers of 512
+constexpr int kHeldLds = 19;  // 152 KB with 512 threads, 76 KB with 256
 typedef __attribute__((address_space(1))) const void* held_gptr_t;
 typedef __attribute__((address_space(3))) void* held_lptr_t;
 
-template <int H, int RM>
-__global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a, int L) {
+template <int NT, int H, int RM>
+__global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
   static_assert(H % 4 == 0 && RM % 4 == 0 && H > RM, "layers go in fours");
-  constexpr int NT = kHeldThreads, WAVES = NT / 64;
+  constexpr int WAVES = NT / 64;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   f32x4* lds = reinterpret_cast<f32x4*>(smem);  // [L][NT]
   __shared__ SoftPart red[WAVES];
   __shared__ GradRow sh;
-  const int row = blockIdx.x, tid = threadIdx.x;
+  const int row = turned_row(blockIdx.x, gridDim.x), tid = threadIdx.x;
   const float* x = a.logits + (size_t)row * a.V;
   float* g = a.grad + (size_t)row * a.V;
   const Span sp(x, 0, a.V);  // (g has the same alignment)
@@ -538,10 +615,14 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a, 
       soft_add<4, false>(p, R, f, a.c);
     }
   }
-  for (int q = rest + RM * NT + tid; q < sp.n4; q += NT) {
-    const f32x4 v = x4[q];
-    const float f[4] = {v[0], v[1], v[2], v[3]};
-    soft_add<4, false>(p, R, f, a.c);
+  for (int at = rest + RM * NT; at < sp.n4; at += 4 * NT) {
+    f32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x4[min(at + i * NT + tid, sp.n4 - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + i * NT + tid >= sp.n4) v[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    add4(v);
   }
   if (tid < sp.outer) {
     const float f[1] = {x[sp.outer_at(tid)]};
@@ -581,7 +662,14 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a, 
       if (rest + i * NT + tid < sp.n4) put(rest + i * NT + tid, r[i]);
   }
   for (int l = 0; l < L; ++l) put((H + l) * NT + tid, lds[l * NT + tid]);
-  for (int q = rest + RM * NT + tid; q < sp.n4; q += NT) put(q, x4[q]);
+  for (int at = rest + RM * NT; at < sp.n4; at += 4 * NT) {
+    f32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x4[min(at + i * NT + tid, sp.n4 - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + i * NT + tid < sp.n4) put(at + i * NT + tid, v[i]);
+  }
   if (tid < sp.outer) {
     const int v = sp.outer_at(tid);
     g[v] = grad_of(x[v], gr, a.c);
@@ -589,20 +677,52 @@ __global__ void __launch_bounds__(kHeldThreads) policy_held_kernel(PolicyDev a, 
   if (tid == sp.owner(y, NT)) g[y] = grad_of(xy, gr, a.c) + gr.coef;
 }
 
-template <int H, int RM>
+template <int NT, int H, int RM>
 static hipError_t launch_held(const PolicyDev& d, int L, hipStream_t s) {
-  auto kern = policy_held_kernel<H, RM>;
+  auto kern = policy_held_kernel<NT, H, RM>;
   if (L > 0) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kHeldLds * kHeldThreads * 16);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kHeldLds * NT * 16);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)d.held), dim3(kHeldThreads), L * kHeldThreads * 16, s, d, L);
+  hipLaunchKernelGGL(kern, dim3((unsigned)d.held), dim3(NT), L * NT * 16, s, d, L);
   return hipGetLastError();
 }
 
-// Whole layers that every held row has at least.
-static int held_layers(int V) { return V < 8 ? 0 : ((V - 6) / 4) / kHeldThreads; }
+// Whole layers of NT groups that every row has at least.
+static int held_layers(int V, int NT) { return V < 8 ? 0 : ((V - 6) / 4) / NT; }
+
+// Rows to hold on chip, and the threads a row: 256 as long as a row fits twice
+// on a compute unit (which then reads one row while it writes another), else
+// 512; 0 threads: rows too short or too long for it.
+static int held_threads(int V) {
+  if (held_layers(V, 256) < 8 || held_layers(V, 512) > kHeldMost) return 0;
+  return held_layers(V, 256) < 48 + kHeldLds + 8 ? 256 : 512;
+}
+static int held_rows(int rows, int V, int num_cu) {
+  const int nt = held_threads(V);
+  if (nt == 256) return rows >= num_cu / 2 ? rows : 0;
+  if (nt == 512) {
+    // one row a compute unit: whole rounds, and a last one that is nearly whole
+    const int rest = rows % num_cu;
+    return 5 * rest >= 3 * num_cu ? rows : rows - rest;
+  }
+  return 0;
+}
+
+static hipError_t launch_held_rows(const PolicyDev& d, hipStream_t s) {
+  if (held_threads(d.V) == 512) {  // (at least 37 layers)
+    const int layers = held_layers(d.V, 512);
+    return layers >= 48 ? launch_held<512, 48, 8>(d, std::min(layers - 48, kHeldLds), s)
+                        : launch_held<512, 36, 12>(d, 0, s);
+  }
+  const int layers = held_layers(d.V, 256);
+  if (layers >= 48) return launch_held<256, 48, 8>(d, std::min(layers - 48, kHeldLds), s);
+  if (layers >= 36) return launch_held<256, 36, 12>(d, 0, s);
+  if (layers >= 24) return launch_held<256, 24, 12>(d, 0, s);
+  if (layers >= 16) return launch_held<256, 16, 8>(d, 0, s);
+  return launch_held<256, 8, 4>(d, std::min(layers - 8, 4), s);
+}
 
 static Base2 base2_factor(double temperature) {
   const double c = 1.4426950408889634 / temperature;
@@ -614,9 +734,9 @@ static Base2 base2_factor(double temperature) {
 // ONCE: the logits are not read again (non-temporal loads)
 template <bool ENT, bool ONCE>
 static void launch_stats(int row0, int rows, int V, int S, Base2 c, const float* logits, const int32_t* tokens,
-                         const float* weights, SoftPart* stats, float* xy, hipStream_t s) {
-  hipLaunchKernelGGL((policy_stats_kernel<ENT, ONCE>), dim3((unsigned)(rows - row0), (unsigned)S), dim3(kPolThreads), 0, s,
-                     row0, V, S, c, logits, tokens, weights, stats, xy);
+                         const float* weights, SoftPart* stats, float* xy, unsigned int* ticket, hipStream_t s) {
+  hipLaunchKernelGGL((policy_stats_kernel<ENT, ONCE>), dim3((unsigned)(rows - row0) * (unsigned)S), dim3(kPolThreads),
+                     0, s, row0, rows, V, S, c, logits, tokens, weights, stats, xy, ticket);
 }
 
 hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
@@ -629,9 +749,9 @@ hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const
   const int rows = B * K;
   const Base2 c = base2_factor(temperature);
   if (entropy)
-    launch_stats<true, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
+    launch_stats<true, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, nullptr, s);
   else
-    launch_stats<false, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, s);
+    launch_stats<false, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, nullptr, s);
   hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((rows + kPolThreads / 32 - 1) / (kPolThreads / 32))),
                      dim3(kPolThreads), 0, s, rows, plan.S, c, 1.0 / temperature, stats, xy, weights, logp, entropy);
   return hipGetLastError();
@@ -648,6 +768,7 @@ hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void*
               0,
               a.V,
               plan.S,
+              1,
               base2_factor(a.temperature),
               1.0 / a.temperature,
               1.0 - a.clip_low,
@@ -662,25 +783,26 @@ hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void*
               stats,
               xy,
               reinterpret_cast<double*>(ws + plan.terms),
+              reinterpret_cast<double*>(ws + plan.sums),
+              reinterpret_cast<unsigned int*>(ws + plan.ticket),
+              1,
               a.loss,
               a.logp,
               a.kl,
               a.grad};
-  const int layers = held_layers(a.V);
-  const bool aligned = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad)) & 15u) == 0;
-  if (a.grad && aligned && layers >= 8) {
-    d.held = rows / num_cu * num_cu;
-    if (d.held) {
-      const hipError_t e = layers >= 48   ? launch_held<48, 8>(d, std::min(layers - 48, kHeldLds), s)
-                           : layers >= 36 ? launch_held<36, 12>(d, 0, s)
-                           : layers >= 24 ? launch_held<24, 12>(d, 0, s)
-                           : layers >= 16 ? launch_held<16, 8>(d, 0, s)
-                                          : launch_held<8, 4>(d, std::min(layers - 8, 4), s);
-      if (e != hipSuccess) return e;
-    }
+  const bool alike = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad)) & 15u) == 0;
+  if (a.grad && alike) d.held = held_rows(rows, a.V, num_cu);
+  if (d.held) {
+    const hipError_t e = launch_held_rows(d, s);
+    if (e != hipSuccess) return e;
   }
-  if (d.held < rows) launch_stats<false, false>(d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, s);
-  const unsigned grid = a.grad ? 1u + (unsigned)(rows - d.held) * (unsigned)plan.S : 1u;
+  if (d.held < rows) launch_stats<false, false>(d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, d.ticket, s);
+  const int left = rows - d.held;
+  d.row_wgs = std::max(1, (left + kRowsPerWg - 1) / kRowsPerWg);
+  // a gradient workgroup brings its row's slices together before it can begin: at
+  // least 4096 entries each, about 5 a compute unit at a time
+  if (left > 0) d.G = std::max(1, std::min((5 * num_cu + left - 1) / left, a.V / 4096));
+  const unsigned grid = (unsigned)d.row_wgs + (a.grad ? (unsigned)left * (unsigned)d.G : 0u);
   hipLaunchKernelGGL(policy_grad_kernel, dim3(grid), dim3(kPolThreads), 0, s, d);
   return hipGetLastError();
 }

@@ -30,6 +30,8 @@ struct PolicyPlan {
   size_t stats;  // byte offset of the [B K][S] partials (max, sum, sum of e t: kPolicyPart bytes)
   size_t xy;     // byte offset of the [B K] float logits of the tokens
   size_t terms;  // byte offset of the [B K] double loss terms of rows held on chip
+  size_t sums;   // byte offset of the [B K] double sums of groups of rows
+  size_t ticket;  // byte offset of a counter of finished workgroups
   size_t total;  // workspace bytes
 };
 
@@ -48,7 +50,9 @@ inline PolicyPlan policy_plan(int B, int K, int V) {
   p.stats = 0;
   p.xy = align256((size_t)rows * p.S * kPolicyPart);
   p.terms = align256(p.xy + (size_t)rows * 4);
-  p.total = align256(p.terms + (size_t)rows * 8);
+  p.sums = align256(p.terms + (size_t)rows * 8);
+  p.ticket = align256(p.sums + (size_t)rows * 8);
+  p.total = p.ticket + 256;
   return p;
 }
 

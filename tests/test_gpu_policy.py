@@ -145,12 +145,12 @@ def test_qwen_vocabulary(dev):
     _check_policy(dev, x, y, old, ref, adv, None)
 
 
-@pytest.mark.parametrize("V", [16390, 17000, 40003, 60001, 75000, 99001, 151936])
+@pytest.mark.parametrize("V", [8200, 8300, 12001, 16390, 17000, 25001, 40003, 60001, 75000, 80003, 99001, 151936, 160001, 204802])
 def test_rows_held_on_chip(dev, V):
     # as many rows as compute units and a few more: each held size, with and without rows left over
     import draft_block_causal_amd as D
 
-    rows = torch.cuda.get_device_properties(dev).multi_processor_count + 3
+    rows = torch.cuda.get_device_properties(dev).multi_processor_count + 13
     log(f"held rows V={V} rows={rows}")
     g = torch.Generator(device=dev).manual_seed(V)
     x = torch.randn((rows, 1, V), generator=g, device=dev) * 2
