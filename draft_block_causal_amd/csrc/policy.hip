@@ -220,6 +220,10 @@ __global__ void __launch_bounds__(kPolThreads)
   int v0, v1;
   row_slice(x, V, sl, S, v0, v1);
   const Span sp(x, v0, v1);
+  // the token's logit, asked for first: at the end it would be two more waits
+  const int y = clamp_id(tokens[row], V);
+  const bool mine = y >= v0 && y < v1;
+  const float x_y = mine ? x[y] : 0.f;
   SoftPart p = kNone;
   float R = ref_of(p.m, c);
   const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
@@ -266,8 +270,7 @@ __global__ void __launch_bounds__(kPolThreads)
   if (far_out(p.m, c)) p = far_out_part<kPolWaves>(x, v0, v1, p.m, c, red);
   if (threadIdx.x == 0) {
     stats[(size_t)row * S + sl] = p;
-    const int y = clamp_id(tokens[row], V);
-    if (y >= v0 && y < v1) xy[row] = x[y];
+    if (mine) xy[row] = x_y;
   }
 }
 
@@ -308,13 +311,14 @@ __global__ void __launch_bounds__(kPolThreads)
   const int row = blockIdx.x * (kPolThreads / 32) + (threadIdx.x >> 5);
   if (row >= rows) return;
   float lp = 0.f, h = 0.f;
-  if (!(weights && weights[row] == 0.f)) {
-    const SoftPart p = row_part(stats, row, S, c);
+  const float x_y = xy[row], w = weights ? weights[row] : 1.f;
+  const SoftPart p = row_part(stats, row, S, c);
+  if (w != 0.f) {
     if (p.s == 0.0) {
       lp = -INFINITY;
     } else {
       const double ln_s = log(p.s);
-      lp = (float)(shift_of(xy[row], p, c, inv_t) - ln_s);
+      lp = (float)(shift_of(x_y, p, c, inv_t) - ln_s);
       h = (float)(ln_s - 0.6931471805599453 * (p.u / p.s));
     }
   }
@@ -345,12 +349,22 @@ struct RowTerms {
   double term, coef;  // weighted loss term; its derivative with respect to logp, over T
 };
 
-__device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, float xy, const SoftPart& p) {
+// What the loss reads of a row, loaded together.  (Rows of weight 0 are read
+// too, and not used.)
+struct RowIn {
+  double w, adv, old, ref;
+};
+
+__device__ __forceinline__ RowIn row_in(const PolicyDev& a, int row) {
+  return RowIn{a.weights ? (double)a.weights[row] : 1.0 / a.rows, a.advantages[row], a.old_logp[row],
+               a.ref_logp ? a.ref_logp[row] : 0.0};
+}
+
+__device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, const RowIn& in, float xy, const SoftPart& p) {
   RowTerms r{-INFINITY, 0.f, 0.0, 0.0};
   if (p.s == 0.0) return r;  // no distribution
   const double lp = shift_of(xy, p, a.c, a.inv_t) - log(p.s);
-  const double w = a.weights ? (double)a.weights[row] : 1.0 / a.rows;
-  const double adv = a.advantages[row], ratio = exp(lp - (double)a.old_logp[row]);
+  const double w = in.w, adv = in.adv, ratio = exp(lp - in.old);
   const bool inside = adv >= 0.0 ? ratio <= a.hi : ratio >= a.lo;
   // (an advantage of 0 stays 0 whatever the ratio)
   double l = 0.0, g = 0.0;
@@ -360,7 +374,7 @@ __device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, int row, float
     if (ratio != ratio) l = g = ratio;
   }
   if (a.ref_logp) {
-    const double d = (double)a.ref_logp[row] - lp, e = expm1(d);
+    const double d = in.ref - lp, e = expm1(d);
     const double kl = d == INFINITY ? INFINITY : e - d;
     r.kl = (float)kl;
     if (a.beta != 0.0) {
@@ -388,8 +402,11 @@ __device__ void policy_rows(const PolicyDev& a) {
   const int row = a.held + (int)blockIdx.x * kRowsPerWg + sub;
   double term = 0.0;
   if (row < a.rows) {
+    const RowIn in = row_in(a, row);
+    const float xy = a.xy[row];
+    const SoftPart p = row_part(a.stats, row, a.S, a.c);
     RowTerms r{0.f, 0.f, 0.0, 0.0};
-    if (!(a.weights && a.weights[row] == 0.f)) r = row_terms(a, row, a.xy[row], row_part(a.stats, row, a.S, a.c));
+    if (in.w != 0.0) r = row_terms(a, in, xy, p);
     term = r.term;
     if (lane == 0) {
       if (a.logp) a.logp[row] = r.logp;
@@ -467,7 +484,10 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
   int v0, v1;
   row_slice(x, a.V, sl, a.G, v0, v1);
   const Span sp(g, v0, v1);
-  if (a.weights && a.weights[row] == 0.f) {  // nothing is read
+  const RowIn in = row_in(a, row);
+  const float xy = a.xy[row];
+  const int y = clamp_id(a.tokens[row], a.V);
+  if (in.w == 0.0) {  // no logit is read
     zero_span<kPolThreads>(g, sp);
     return;
   }
@@ -482,10 +502,9 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
     __builtin_amdgcn_sched_barrier(0);
   };
   if (alike && sp.n4 > 0) load(0);
-  const float xy = a.xy[row];
   if (threadIdx.x < 32) {
     const SoftPart p = row_part(a.stats, row, a.S, a.c);
-    const RowTerms r = row_terms(a, row, xy, p);
+    const RowTerms r = row_terms(a, in, xy, p);
     if (threadIdx.x == 0) sh = grad_row(r, p, a.c);
   }
   __syncthreads();
@@ -494,7 +513,6 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
     zero_span<kPolThreads>(g, sp);
     return;
   }
-  const int y = clamp_id(a.tokens[row], a.V);
   if (alike) {
     for (int at = 0; at < sp.n4; at += kStep) {
       if (at > 0) load(at);
@@ -547,7 +565,8 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
   const float* x = a.logits + (size_t)row * a.V;
   float* g = a.grad + (size_t)row * a.V;
   const Span sp(x, 0, a.V);  // (g has the same alignment)
-  if (a.weights && a.weights[row] == 0.f) {
+  const RowIn in = row_in(a, row);
+  if (in.w == 0.0) {
     zero_span<NT>(g, sp);
     if (tid == 0) {
       if (a.logp) a.logp[row] = 0.f;
@@ -631,7 +650,7 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
   p = block_soft<WAVES>(p, red, a.c);
   if (far_out(p.m, a.c)) p = far_out_part<WAVES>(x, 0, a.V, p.m, a.c, red);
   if (tid < 64) {
-    const RowTerms r = row_terms(a, row, xy, p);
+    const RowTerms r = row_terms(a, in, xy, p);
     if (tid == 0) {
       if (a.logp) a.logp[row] = r.logp;
       if (a.kl) a.kl[row] = r.kl;
