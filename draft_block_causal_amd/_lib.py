@@ -8,6 +8,7 @@ raise if the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -502,41 +503,36 @@ def _take(t: torch.Tensor, name: str, dtype, shape, index: int, device) -> int:
     return t.data_ptr()
 
 
-def _gpu(t: torch.Tensor, name: str) -> torch.device:
+def _gpu_index(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    return t.device
+    return t.get_device()
 
 
-class _On:
-    """The device of a call's tensors made current, and the call's stream: the
-    given one, else the device's current one.  What is allocated inside belongs
-    to that stream, so scratch memory that is freed when the call returns is
-    not handed out again before the call's kernels are done with it."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("dev", "stream", "prev")
 
-    def __init__(self, dev: torch.device, stream=None):
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        self.dev, self.stream = dev, stream
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call has to make its device or stream current first (`_on`)."""
+    return stream is not None or torch.cuda.current_device() != index
 
-    def __enter__(self):
-        self.prev = None
-        if self.stream is not None:
-            self.prev = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.dev.index:
-            self.prev = torch.cuda.device(self.dev)
-        else:
-            return torch._C._cuda_getCurrentRawStream(self.dev.index)
-        self.prev.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
 
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            self.prev.__exit__(*exc)
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """The call's stream (or, without one, its device) made current.  What is
+    allocated inside belongs to that stream, so scratch memory that is freed when
+    the call returns is not handed out again before the call's kernels are done
+    with it."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        with torch.cuda.stream(stream):
+            yield
 
 
 def _scratch(workspace: Optional[torch.Tensor], need, sizes, dev) -> torch.Tensor:
@@ -552,20 +548,26 @@ def domino_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scal
     """x [..., cols] (float32 or bfloat16) in 8 bits with one scale a row; returns
     (q int8 like x, scale float32 [...]).  An LM head gets a scale per channel,
     hidden states one per token."""
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    i, dev, dt = _gpu_index(x, "x"), x.device, x.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be float32 or bfloat16, got {dt}")
     if x.dim() < 1:
         raise ValueError("x must be [..., cols]")
-    shape, i, dev = x.shape, x.get_device(), _gpu(x, "x")
-    px, cols, outer = _take(x, "x", x.dtype, shape, i, dev), shape[-1], shape[:-1]
-    with _On(dev, stream) as st:
-        if q is None:
-            q = torch.empty(shape, dtype=torch.int8, device=dev)
-        if scale is None:
-            scale = torch.empty(outer, dtype=torch.float32, device=dev)
-        _check("domino_quantize_rows", load_library().domino_quantize_rows(
-            outer.numel(), cols, DOMINO_BF16 if x.dtype is torch.bfloat16 else DOMINO_F32, px,
-            _take(q, "q", torch.int8, shape, i, dev), _take(scale, "scale", torch.float32, outer, i, dev), st))
+    if _elsewhere(i, stream):
+        with _on(dev, stream):
+            return domino_quantize_rows(x, q, scale)
+    shape = x.shape
+    cols, outer = shape[-1], shape[:-1]
+    px = _take(x, "x", dt, shape, i, dev)
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(outer, dtype=torch.float32, device=dev)
+    status = (_lib or load_library()).domino_quantize_rows(
+        outer.numel(), cols, DOMINO_BF16 if dt is torch.bfloat16 else DOMINO_F32, px,
+        _take(q, "q", torch.int8, shape, i, dev), _take(scale, "scale", torch.float32, outer, i, dev), _raw_stream(i))
+    if status:
+        _check("domino_quantize_rows", status)
     return q, scale
 
 
@@ -574,20 +576,24 @@ def domino_base_logits_i8(hidden_q: torch.Tensor, hidden_scale: torch.Tensor, lm
                           stream=None) -> torch.Tensor:
     """Base logits [batch, block, vocab] from hidden states [batch, block, d] and an LM
     head [vocab, d] in 8 bits (domino_quantize_rows)."""
+    i, dev = _gpu_index(lm_head_q, "lm_head_q"), lm_head_q.device
     if hidden_q.dim() != 3 or lm_head_q.dim() != 2:
         raise ValueError("hidden_q must be [batch, block, d] and lm_head_q [vocab, d]")
+    if _elsewhere(i, stream):
+        with _on(dev, stream):
+            return domino_base_logits_i8(hidden_q, hidden_scale, lm_head_q, lm_head_scale, base_logits)
     B, K, d = hidden_q.shape
-    V = lm_head_q.shape[0]
-    i, i8, f32, dev = lm_head_q.get_device(), torch.int8, torch.float32, lm_head_q.device
+    V, i8, f32 = lm_head_q.shape[0], torch.int8, torch.float32
     hq = _take(hidden_q, "hidden_q", i8, (B, K, d), i, dev)
     hs = _take(hidden_scale, "hidden_scale", f32, (B, K), i, dev)
     wq = _take(lm_head_q, "lm_head_q", i8, (V, d), i, dev)
     ws = _take(lm_head_scale, "lm_head_scale", f32, (V,), i, dev)
-    with _On(_gpu(lm_head_q, "lm_head_q"), stream) as st:
-        if base_logits is None:
-            base_logits = torch.empty((B, K, V), dtype=f32, device=dev)
-        _check("domino_base_logits_i8", load_library().domino_base_logits_i8(
-            B, K, d, V, hq, hs, wq, ws, _take(base_logits, "base_logits", f32, (B, K, V), i, dev), st))
+    if base_logits is None:
+        base_logits = torch.empty((B, K, V), dtype=f32, device=dev)
+    status = (_lib or load_library()).domino_base_logits_i8(
+        B, K, d, V, hq, hs, wq, ws, _take(base_logits, "base_logits", f32, (B, K, V), i, dev), _raw_stream(i))
+    if status:
+        _check("domino_base_logits_i8", status)
     return base_logits
 
 
@@ -601,20 +607,26 @@ def domino_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperatur
                           stream=None) -> torch.Tensor:
     """log softmax(logits / T) at each position's token, [batch, block]; the entropy of
     each position is written when a tensor is given.  Positions of weight 0 are not read."""
+    i, dev = _gpu_index(logits, "logits"), logits.device
     if logits.dim() != 3:
         raise ValueError("logits must be [batch, block, vocab]")
-    B, K, V = logits.shape
-    i, f32, dev, rows = logits.get_device(), torch.float32, logits.device, (B, K)
-    x = _take(logits, "logits", f32, (B, K, V), i, dev)
+    if _elsewhere(i, stream):
+        with _on(dev, stream):
+            return domino_token_logprobs(logits, tokens, temperature, weights, logp, entropy, workspace)
+    B, K, V = shape = logits.shape
+    f32, rows = torch.float32, (B, K)
+    x = _take(logits, "logits", f32, shape, i, dev)
     y = _take(tokens, "tokens", torch.int32, rows, i, dev)
     w = None if weights is None else _take(weights, "weights", f32, rows, i, dev)
     h = None if entropy is None else _take(entropy, "entropy", f32, rows, i, dev)
-    with _On(_gpu(logits, "logits"), stream) as st:
-        if logp is None:
-            logp = torch.empty(rows, dtype=f32, device=dev)
-        ws = _scratch(workspace, domino_token_logprobs_workspace_size, (B, K, V), dev)
-        _check("domino_token_logprobs", load_library().domino_token_logprobs(
-            B, K, V, x, y, w, temperature, _take(logp, "logp", f32, rows, i, dev), h, ws.data_ptr(), ws.numel(), st))
+    if logp is None:
+        logp = torch.empty(rows, dtype=f32, device=dev)
+    ws = _scratch(workspace, domino_token_logprobs_workspace_size, (B, K, V), dev)
+    status = (_lib or load_library()).domino_token_logprobs(
+        B, K, V, x, y, w, temperature, _take(logp, "logp", f32, rows, i, dev), h, ws.data_ptr(), ws.numel(),
+        _raw_stream(i))
+    if status:
+        _check("domino_token_logprobs", status)
     return logp
 
 
@@ -633,11 +645,16 @@ def domino_policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: tor
     positions' log-probabilities and divergences and the gradient of the logits are
     written when given (grad may be the logits themselves).  The weights carry the mask
     and the normalisation; None is 1 / (batch * block) everywhere."""
+    i, dev = _gpu_index(logits, "logits"), logits.device
     if logits.dim() != 3:
         raise ValueError("logits must be [batch, block, vocab]")
-    B, K, V = logits.shape
-    i, f32, dev, rows = logits.get_device(), torch.float32, logits.device, (B, K)
-    x = _take(logits, "logits", f32, (B, K, V), i, dev)
+    if _elsewhere(i, stream):
+        with _on(dev, stream):
+            return domino_policy_loss(logits, tokens, old_logp, advantages, clip_low, clip_high, kl_coef, ref_logp,
+                                      weights, temperature, loss, logp, kl, grad, workspace)
+    B, K, V = shape = logits.shape
+    f32, rows = torch.float32, (B, K)
+    x = _take(logits, "logits", f32, shape, i, dev)
     y = _take(tokens, "tokens", torch.int32, rows, i, dev)
     old = _take(old_logp, "old_logp", f32, rows, i, dev)
     adv = _take(advantages, "advantages", f32, rows, i, dev)
@@ -645,14 +662,15 @@ def domino_policy_loss(logits: torch.Tensor, tokens: torch.Tensor, old_logp: tor
     w = None if weights is None else _take(weights, "weights", f32, rows, i, dev)
     lp = None if logp is None else _take(logp, "logp", f32, rows, i, dev)
     k = None if kl is None else _take(kl, "kl", f32, rows, i, dev)
-    g = None if grad is None else _take(grad, "grad", f32, (B, K, V), i, dev)
-    with _On(_gpu(logits, "logits"), stream) as st:
-        if loss is None:
-            loss = torch.zeros((1,), dtype=f32, device=dev)
-        ws = _scratch(workspace, domino_policy_loss_workspace_size, (B, K, V), dev)
-        _check("domino_policy_loss", load_library().domino_policy_loss(
-            B, K, V, x, y, old, ref, adv, w, temperature, clip_low, clip_high, kl_coef,
-            _take(loss, "loss", f32, (1,), i, dev), lp, k, g, ws.data_ptr(), ws.numel(), st))
+    g = None if grad is None else _take(grad, "grad", f32, shape, i, dev)
+    if loss is None:
+        loss = torch.zeros((1,), dtype=f32, device=dev)
+    ws = _scratch(workspace, domino_policy_loss_workspace_size, (B, K, V), dev)
+    status = (_lib or load_library()).domino_policy_loss(
+        B, K, V, x, y, old, ref, adv, w, temperature, clip_low, clip_high, kl_coef,
+        _take(loss, "loss", f32, (1,), i, dev), lp, k, g, ws.data_ptr(), ws.numel(), _raw_stream(i))
+    if status:
+        _check("domino_policy_loss", status)
     return loss
 
 

@@ -120,27 +120,16 @@ def test_valid_calls_without_gpu_report_hip_error(lib):
     assert _policy(lib, ref=None, beta=0.0, w=None, logp=None, kl=None, grad=None) == E_HIP
 
 
-def test_binding_refuses_wrong_tensors():
-    f32, i32 = torch.float32, torch.int32
+def test_binding_refuses_tensors_that_are_not_on_a_gpu():
     z = torch.zeros
+    with pytest.raises(ValueError, match="on a GPU"):
+        D.domino_quantize_rows(z((2, 64)))
+    with pytest.raises(ValueError, match="on a GPU"):
+        D.domino_base_logits_i8(z((1, 2, 64), dtype=torch.int8), z((1, 2)), z((9, 64), dtype=torch.int8), z(9))
+    x, y = z((2, 3, 7)), z((2, 3), dtype=torch.int32)
+    with pytest.raises(ValueError, match="on a GPU"):
+        D.domino_token_logprobs(x, y)
+    with pytest.raises(ValueError, match="on a GPU"):
+        D.domino_policy_loss(x, y, z((2, 3)), z((2, 3)))
     with pytest.raises(TypeError):
-        D.domino_quantize_rows(z((2, 64), dtype=torch.float16))
-    with pytest.raises(ValueError):
-        D.domino_quantize_rows(z((64, 2)).t())
-    with pytest.raises(ValueError):
-        D.domino_quantize_rows(z((2, 64)))  # not on a GPU
-    with pytest.raises(TypeError):
-        D.domino_base_logits_i8(z((1, 2, 64)), z((1, 2)), z((9, 64), dtype=torch.int8), z(9))
-    with pytest.raises(ValueError):
-        D.domino_base_logits_i8(z((1, 2, 64), dtype=torch.int8), z((1, 2)), z((9, 32), dtype=torch.int8), z(9))
-    x, y = z((2, 3, 7), dtype=f32), z((2, 3), dtype=i32)
-    with pytest.raises(ValueError):
-        D.domino_token_logprobs(x[0], y)
-    with pytest.raises(TypeError):
-        D.domino_token_logprobs(x, y.long())
-    with pytest.raises(ValueError):
-        D.domino_token_logprobs(x, y, weights=z(3))
-    with pytest.raises(TypeError):
-        D.domino_policy_loss(x.bfloat16(), y, z((2, 3)), z((2, 3)))
-    with pytest.raises(ValueError):
-        D.domino_policy_loss(x, y, z((2, 3)), z((2, 3)), grad=z((2, 3, 8)))
+        D.domino_quantize_rows([[1.0] * 32])

@@ -464,3 +464,50 @@ def test_roll_out_and_policy_step(dev, target_seed):
     room = (hidden.abs().sum(-1).max() * ws.max() / 2 + hs.max() * head.tensors["lm_head"].abs().sum(-1).max() / 2
             + w.d * hs.max() * ws.max() / 4).item()
     assert np.isfinite(n(old)).all() and np.abs(n(logp) - n(old))[live].max() < 2 * room + 1e-4
+
+
+def test_binding_refuses_wrong_tensors(dev):
+    import draft_block_causal_amd as D
+
+    def z(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype, device=dev)
+
+    i8, i32 = torch.int8, torch.int32
+    with pytest.raises(TypeError):
+        D.domino_quantize_rows(z(2, 64, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        D.domino_quantize_rows(z(64, 2).t())  # not contiguous
+    with pytest.raises(ValueError):
+        D.domino_quantize_rows(z(2, 64), q=z(2, 32, dtype=i8))
+    with pytest.raises(D.DominoError):
+        D.domino_quantize_rows(z(2, 40))
+    with pytest.raises(TypeError):
+        D.domino_base_logits_i8(z(1, 2, 64), z(1, 2), z(9, 64, dtype=i8), z(9))
+    with pytest.raises(ValueError):
+        D.domino_base_logits_i8(z(1, 2, 64, dtype=i8), z(1, 2), z(9, 32, dtype=i8), z(9))
+    with pytest.raises(ValueError):
+        D.domino_base_logits_i8(z(2, 64, dtype=i8), z(2), z(9, 64, dtype=i8), z(9))
+    x, y = z(2, 3, 7), z(2, 3, dtype=i32)
+    with pytest.raises(ValueError):
+        D.domino_token_logprobs(x[0], y)
+    with pytest.raises(TypeError):
+        D.domino_token_logprobs(x, y.long())
+    with pytest.raises(ValueError):
+        D.domino_token_logprobs(x, y, weights=z(3))
+    with pytest.raises(ValueError):
+        D.domino_token_logprobs(x, y.cpu())
+    with pytest.raises(D.DominoError):
+        D.domino_token_logprobs(x, y, temperature=0.0)
+    with pytest.raises(D.DominoError):
+        D.domino_token_logprobs(x, y, workspace=z(16, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        D.domino_token_logprobs(x, y, workspace=z(1 << 16))
+    with pytest.raises(TypeError):
+        D.domino_policy_loss(x.bfloat16(), y, z(2, 3), z(2, 3))
+    with pytest.raises(ValueError):
+        D.domino_policy_loss(x, y, z(2, 3), z(2, 3), grad=z(2, 3, 8))
+    with pytest.raises(D.DominoError):
+        D.domino_policy_loss(x, y, z(2, 3), z(2, 3), kl_coef=0.1)  # no reference
+    old = z(2, 3)
+    with pytest.raises(D.DominoError):
+        D.domino_policy_loss(x, y, old, z(2, 3), logp=old)  # an output over an input
