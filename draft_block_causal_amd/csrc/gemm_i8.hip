@@ -227,7 +227,7 @@ static hipError_t launch_stream(const int8_t* A, const float* as, int M, const i
 }
 
 // ---------------------------------------------------------------------------
-// Tiled kernel: BM x 256 outputs a tile, 8 waves (a 2 x 4 grid), one workgroup
+// Tiled kernel: BM x BN outputs a tile, 8 waves (a 2 x 4 grid), one workgroup
 // a compute unit that walks its tiles without a break: the loads of the next
 // tile are in flight while the last one's results are stored.
 // Operands go from memory straight into LDS (16 bytes a lane), in steps of 128
@@ -258,26 +258,30 @@ typedef __attribute__((address_space(3))) void* lptr_t;
 
 __device__ const unsigned char kZeros[16] = {};  // what A reads past K
 
-template <int BM, int WS, int AS>
+template <int BM, int BN, int WS, int AS>
 struct TileI8 {
-  static constexpr int kThreads = 512, kBN = 256, kRow = 128;
+  static constexpr int kThreads = 512, kBN = BN, kRow = 128;
   static constexpr int kABytes = BM * kRow, kWBytes = kBN * kRow;
-  static constexpr int kLds = WS * kWBytes + AS * kABytes;
+  static constexpr int kRings = WS * kWBytes + AS * kABytes;
+  // scales of a tile, in LDS where there is room (two tiles' in turn)
+  static constexpr bool kScalesInLds = kRings + 2 * (BM + BN) * 4 <= 160 * 1024;
+  static constexpr int kLds = kRings + (kScalesInLds ? 2 * (BM + BN) * 4 : 0);
+  static constexpr int kStores = BM / 2 / 16 * (BN / 4 / 16);  // of a whole tile, per wave
   static constexpr int kAL = BM / 32, kWL = kBN / 32;  // loads of a step per loading wave
   static constexpr int kFA = BM / 2 / 16, kFW = kBN / 4 / 16;
-  static_assert(BM % 128 == 0 && WS >= 2 && AS >= 2 && (WS - 2) * kWL < 64 && (AS - 2) * kAL < 64, "rings");
+  static_assert(BM % 128 == 0 && BN % 64 == 0 && WS >= 2 && AS >= 2 && (WS - 2) * kWL < 64 && (AS - 2) * kAL < 64, "rings");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 // vmcnt(n), lgkmcnt(0); expcnt at its maximum
 #define DOMINO_I8_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | 0x0070)
 
-template <int BM, int WS, int AS>
+template <int BM, int BN, int WS, int AS>
 __global__ void __launch_bounds__(512, 1)
     gemm_i8_tiled_kernel(const int8_t* __restrict__ A, const float* __restrict__ as, int M,
                          const int8_t* __restrict__ W, const float* __restrict__ ws, int N, int K,
                          float* __restrict__ C, int num_m, int num_n) {
-  using T = TileI8<BM, WS, AS>;
+  using T = TileI8<BM, BN, WS, AS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, col = lane & 15;
   const int wm = wave >> 2, wn = wave & 3;
@@ -348,12 +352,33 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
     for (int j = 0; j < T::kFW; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-  // The tile's scales: loaded at its start, taken (the empty asm) behind a wait
-  // that the operands need anyway.  Loaded where they are used, every store
-  // would wait for the loads in flight.
+  // The tile's scales: loaded at its start, into LDS where there is room, else
+  // into registers that are taken (the empty asm) behind a wait that the operands
+  // need anyway.  Loaded where they are used, every store would wait for the loads
+  // in flight.
   float sn[T::kFW][4], sm[T::kFA];
   int m0, n0;
-  auto scales = [&]() {
+  float* lds_scales = reinterpret_cast<float*>(smem + T::kRings);  // [2][BN of ws, BM of as]
+  auto scales = [&](int parity) {
+    if constexpr (T::kScalesInLds) {
+      // 64 scales a load, dealt out to the waves that load the operand
+      float* dst = lds_scales + parity * (BM + BN);
+      const int w = wave & 3;
+      if (loads_w) {
+#pragma unroll
+        for (int i = 0; i < BN / 64; ++i)
+          if (i % 4 == w)
+            __builtin_amdgcn_global_load_lds((gptr_t)(ws + min(n0 + i * 64 + lane, N - 1)), (lptr_t)(dst + i * 64), 4, 0,
+                                             0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < BM / 64; ++i)
+          if (i % 4 == w)
+            __builtin_amdgcn_global_load_lds((gptr_t)(as + min(m0 + i * 64 + lane, M - 1)), (lptr_t)(dst + BN + i * 64),
+                                             4, 0, 0);
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < T::kFW; ++j)
 #pragma unroll
@@ -362,6 +387,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; i < T::kFA; ++i) sm[i] = as[min(m0 + (wm * T::kFA + i) * 16 + col, M - 1)];
   };
   auto take_scales = [&]() {
+    if constexpr (T::kScalesInLds) return;
 #pragma unroll
     for (int j = 0; j < T::kFW; ++j)
 #pragma unroll
@@ -370,7 +396,20 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; i < T::kFA; ++i) asm volatile("" : "+v"(sm[i]));
   };
   const bool vec = (N & 3) == 0;  // then every group of 4 columns is 16-byte aligned and whole
-  auto store = [&]() {
+  // Whether every store of the tile was made: the count of loads in flight that
+  // a wave may wait for includes its stores.
+  auto store = [&](int parity) {
+    if constexpr (T::kScalesInLds) {
+      const float* src = lds_scales + parity * (BM + BN);
+#pragma unroll
+      for (int j = 0; j < T::kFW; ++j) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(src + (wn * T::kFW + j) * 16 + grp * 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sn[j][q] = v[q];
+      }
+#pragma unroll
+      for (int i = 0; i < T::kFA; ++i) sm[i] = src[BN + (wm * T::kFA + i) * 16 + col];
+    }
     if (vec && m0 + BM <= M && n0 + T::kBN <= N) {  // a whole tile
       float* c = C + (size_t)(m0 + wm * T::kFA * 16 + col) * N + n0 + wn * T::kFW * 16 + grp * 4;
 #pragma unroll
@@ -385,7 +424,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         c += (size_t)16 * N;
       }
-      return;
+      return true;
     }
 #pragma unroll
     for (int i = 0; i < T::kFA; ++i) {
@@ -409,6 +448,7 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
     }
+    return false;
   };
 
   seek();
@@ -421,6 +461,7 @@ __global__ void __launch_bounds__(512, 1)
 
   int d = 0, tile = 0, sa_slot = 0, sw_slot = 0;
   tile_at(0, m0, n0);
+  bool stored = false;  // the step before stored a whole tile
   for (int g = 0; g < total; ++g) {
     const unsigned char* sW = smem + sw_slot * T::kWBytes + wn * T::kFW * 2048 + col * 128;
     const unsigned char* sA = smem + WS * T::kWBytes + sa_slot * T::kABytes + wm * T::kFA * 2048 + col * 128;
@@ -434,13 +475,31 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int i = 0; i < T::kFA; ++i) af[i] = ld16(sA + i * 2048 + slot);
       if (h == 0) {
-        if (d == 0) scales();
+        if (d == 0) scales(tile & 1);
         if (g + ahead < total) issue();
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        if (T::kScalesInLds && nd == 1) {
+          // a tile of one step: the first row of waves stores while the second is
+          // still reading, so the scales have to be there by now
+          if (g + ahead >= total)
+            DOMINO_I8_WAIT(0);
+          else if (loads_w)
+            DOMINO_I8_WAIT(T::kWL);
+          else
+            DOMINO_I8_WAIT(T::kAL);
+        } else {
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        }
       } else if (loads_w && g + WS - 1 < total) {
-        DOMINO_I8_WAIT((WS - 2) * T::kWL);
+        // (step g + 1's loads were issued before the stores where the ring is deeper than 2)
+        if (WS > 2 && T::kScalesInLds && stored)
+          DOMINO_I8_WAIT((WS - 2) * T::kWL + T::kStores);
+        else
+          DOMINO_I8_WAIT((WS - 2) * T::kWL);
       } else if (!loads_w && g + AS - 1 < total) {
-        DOMINO_I8_WAIT((AS - 2) * T::kAL);
+        if (AS > 2 && T::kScalesInLds && stored)
+          DOMINO_I8_WAIT((AS - 2) * T::kAL + T::kStores);
+        else
+          DOMINO_I8_WAIT((AS - 2) * T::kAL);
       } else {
         DOMINO_I8_WAIT(0);
       }
@@ -453,7 +512,10 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int j = 0; j < T::kFW; ++j) acc[i][j] = mma16_i8(acc[i][j], wf[j], af[i]);
       __builtin_amdgcn_sched_barrier(0);
-      if (h == 1 && d == nd - 1) store();
+      // (a wait that leaves out the stores also leaves out the next tile's scales,
+      // which the second row of waves then has only at the end of step 1, while the
+      // first may store at the end of a tile of two)
+      if (h == 1) stored = d == nd - 1 && store(tile & 1) && nd > 2;
       __builtin_amdgcn_s_barrier();
     }
     if (++sa_slot == AS) sa_slot = 0;
@@ -466,14 +528,14 @@ __global__ void __launch_bounds__(512, 1)
   if (wm == 0) __builtin_amdgcn_s_barrier();  // equal barrier counts in both rows of waves
 }
 
-template <int BM, int WS, int AS>
+template <int BM, int BN, int WS, int AS>
 static hipError_t launch_tiled(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
                                float* C, int num_cu, hipStream_t s) {
-  using T = TileI8<BM, WS, AS>;
+  using T = TileI8<BM, BN, WS, AS>;
   const int num_m = (M + BM - 1) / BM, num_n = (N + T::kBN - 1) / T::kBN;
   // a multiple of 8 workgroups, at most one a compute unit
   const int want = (num_n + 7) / 8 * num_m, have = std::max(1, num_cu / 8);
-  auto kern = gemm_i8_tiled_kernel<BM, WS, AS>;
+  auto kern = gemm_i8_tiled_kernel<BM, BN, WS, AS>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), T::kLds, done);
   if (e != hipSuccess) return e;
@@ -498,8 +560,13 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
     return launch_stream<8, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
   }
   if (M <= 16) return launch_stream_g<16, 8, 1>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
-  return M <= 128 ? launch_tiled<128, 3, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
-                  : launch_tiled<256, 2, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  if (M > 128) return launch_tiled<256, 256, 2, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  // One M tile: 256 or 320 columns a tile, whichever leaves a compute unit fewer
+  // columns in all (Qwen3 vocabulary on 256 compute units: 3 rounds of 256 or 2 of
+  // 320; 128 rows, d = 2560: 113 and 105 us, d = 4096: 147 and 150 us).
+  auto columns = [&](int bn) { return ((N + bn - 1) / bn + num_cu - 1) / num_cu * bn; };
+  return columns(320) < columns(256) ? launch_tiled<128, 320, 3, 2>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
+                                     : launch_tiled<128, 256, 3, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
 }
 
 }  // namespace domino

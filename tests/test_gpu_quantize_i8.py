@@ -133,13 +133,16 @@ def test_base_logits_i8_largest_sums(dev, B, K):
     _logits_case(dev, B, K, 8192, 65, full=-128)
 
 
-@pytest.mark.parametrize("B", [1, 4, 8, 20])
-def test_base_logits_i8_over_the_whole_vocabulary(dev, B):
-    # Qwen3 vocabulary: many tiles per workgroup; checked on every 37th column against the oracle, and two calls agree
+@pytest.mark.parametrize("B,d,V", [(1, 512, 151936), (4, 512, 151936), (8, 512, 151936), (20, 512, 151936),
+                                   (5, 32, 151936), (8, 128, 151936), (7, 160, 220000), (8, 256, 300004), (8, 64, 65536),
+                                   (12, 64, 151936), (16, 128, 220001), (3, 64, 500000), (1, 96, 999999)])
+def test_base_logits_i8_over_a_whole_vocabulary(dev, B, d, V):
+    # many tiles per workgroup, down to one step of K each; checked on every 37th column against the oracle, and two
+    # calls agree
     import draft_block_causal_amd as D
 
-    K, d, V = 16, 512, 151936
-    log(f"base_logits_i8 whole vocabulary B={B}")
+    K = 16
+    log(f"base_logits_i8 whole vocabulary B={B} d={d} V={V}")
     rng = np.random.default_rng(B)
     hq, wq = _i8(rng, B, K, d), _i8(rng, V, d)
     hs, ws = rng.uniform(0.01, 0.02, (B, K)).astype(np.float32), rng.uniform(0.01, 0.02, V).astype(np.float32)
