@@ -356,8 +356,10 @@ extern "C" int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab
   int st = domino::check_logprobs_args(batch, block, vocab, logits, tokens, weights, temperature, logp, entropy,
                                        workspace, workspace_bytes);
   if (st != DOMINO_OK || batch == 0) return st;
+  const int num_cu = device_cu_count();
+  if (num_cu <= 0) return DOMINO_ERR_HIP;
   return hip_status(domino::launch_token_logprobs(batch, block, vocab, logits, tokens, weights, temperature, logp,
-                                                  entropy, domino::policy_plan(batch, block, vocab), workspace,
+                                                  entropy, domino::policy_plan(batch, block, vocab), workspace, num_cu,
                                                   static_cast<hipStream_t>(stream)));
 }
 

@@ -378,7 +378,7 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
 // the workspace follows policy_plan(B, K, V).
 hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
                                  double temperature, float* logp, float* entropy, const PolicyPlan& plan,
-                                 void* workspace, hipStream_t s);
+                                 void* workspace, int num_cu, hipStream_t s);
 hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void* workspace, int num_cu,
                               hipStream_t s);
 

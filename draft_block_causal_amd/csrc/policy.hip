@@ -194,48 +194,22 @@ __device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 
   return p;
 }
 
-// Row of workgroup b of n when a workgroup takes a row: groups of 8 consecutive
-// rows are turned against the 8 XCDs that workgroups go round, each group by
-// another step, so that positions of a block that are often masked (its last
-// ones) do not all fall to the same XCD.
-__device__ __forceinline__ int turned_row(int b, int n) {
-  return (b | 7) < n ? (b & ~7) | ((b + (b >> 3) + (b >> 4)) & 7) : b;
-}
-
-// Workgroup b: slice b % S of row b / S, so that neighbouring slices go to
-// different XCDs (64 blocks cut at their acceptance lengths: with all slices of
-// a row on one XCD 70 us, the XCD of a block's first positions having 1.4 times
-// the average work; POLXCD us).
-template <bool ENT, bool ONCE>
-__global__ void __launch_bounds__(kPolThreads)
-    policy_stats_kernel(int row0, int rows, int V, int S, Base2 c, const float* __restrict__ logits,
-                        const int32_t* __restrict__ tokens, const float* __restrict__ weights,
-                        SoftPart* __restrict__ stats, float* __restrict__ xy,
-                        unsigned int* __restrict__ ticket) {
-  __shared__ SoftPart red[kPolWaves];
-  if (blockIdx.x == 0 && threadIdx.x == 0 && ticket) *ticket = 0;  // for policy_grad_kernel
-  const int sl = (int)(blockIdx.x % (unsigned)S), row = row0 + turned_row((int)(blockIdx.x / (unsigned)S), rows - row0);
-  if (weights && weights[row] == 0.f) return;
-  const float* x = logits + (size_t)row * V;
-  int v0, v1;
-  row_slice(x, V, sl, S, v0, v1);
-  const Span sp(x, v0, v1);
-  // the token's logit, asked for first: at the end it would be two more waits
-  const int y = clamp_id(tokens[row], V);
-  const bool mine = y >= v0 && y < v1;
-  const float x_y = mine ? x[y] : 0.f;
+// The part of a span of a row, taken by a workgroup of NT threads (red: one entry
+// per wave); the result in every thread.
+template <int NT, bool ENT, bool ONCE>
+__device__ __forceinline__ SoftPart span_soft(const float* x, const Span& sp, Base2 c, SoftPart* red) {
   SoftPart p = kNone;
   float R = ref_of(p.m, c);
   const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
   {
     // four groups a thread and step, the next step in flight while one is used;
     // the last step may be ragged
-    constexpr int U = 4, kStep = U * kPolThreads;
+    constexpr int U = 4, kStep = U * NT;
     const int n = (sp.n4 + kStep - 1) / kStep;
     auto load = [&](f32x4 (&d)[U], int step) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const f32x4* at = x4 + min(step * kStep + i * kPolThreads + (int)threadIdx.x, sp.n4 - 1);
+        const f32x4* at = x4 + min(step * kStep + i * NT + (int)threadIdx.x, sp.n4 - 1);
         d[i] = ONCE ? __builtin_nontemporal_load(at) : *at;
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -244,7 +218,7 @@ __global__ void __launch_bounds__(kPolThreads)
       if ((step + 1) * kStep > sp.n4) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-          if (step * kStep + i * kPolThreads + (int)threadIdx.x >= sp.n4)
+          if (step * kStep + i * NT + (int)threadIdx.x >= sp.n4)
             d[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       }
       float f[4 * U];
@@ -266,11 +240,54 @@ __global__ void __launch_bounds__(kPolThreads)
     const float f[1] = {x[sp.outer_at(threadIdx.x)]};
     soft_add<1, ENT>(p, R, f, c);
   }
-  p = block_soft<kPolWaves>(p, red, c);
-  if (far_out(p.m, c)) p = far_out_part<kPolWaves>(x, v0, v1, p.m, c, red);
+  p = block_soft<NT / 64>(p, red, c);
+  if (far_out(p.m, c)) p = far_out_part<NT / 64>(x, sp.v0, sp.v1, p.m, c, red);
+  return p;
+}
+
+// Row of workgroup b of n when a workgroup takes a row: groups of 8 consecutive
+// rows are turned against the 8 XCDs that workgroups go round, each group by
+// another step, so that positions of a block that are often masked (its last
+// ones) do not all fall to the same XCD.
+__device__ __forceinline__ int turned_row(int b, int n) {
+  return (b | 7) < n ? (b & ~7) | ((b + (b >> 3) + (b >> 4)) & 7) : b;
+}
+
+// Workgroup b: slice b % S of row b / S, so that neighbouring slices go to
+// different XCDs (64 blocks cut at their acceptance lengths: with all slices of
+// a row on one XCD 70 us, the XCD of a block's first positions having 1.4 times
+// the average work; POLXCD us).
+// ONCE: the logits are not read again (non-temporal loads).
+struct StatsDev {
+  int row0, rows, V, S;
+  Base2 c;
+  const float* logits;
+  const int32_t* tokens;
+  const float* weights;
+  SoftPart* stats;
+  float* xy;
+  unsigned int* ticket;  // cleared for policy_grad_kernel, if not null
+};
+
+template <bool ENT, bool ONCE>
+__global__ void __launch_bounds__(kPolThreads) policy_stats_kernel(StatsDev a) {
+  __shared__ SoftPart red[kPolWaves];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.ticket) *a.ticket = 0;
+  const int V = a.V, S = a.S;
+  const int sl = (int)(blockIdx.x % (unsigned)S), row = a.row0 + turned_row((int)(blockIdx.x / (unsigned)S), a.rows - a.row0);
+  if (a.weights && a.weights[row] == 0.f) return;
+  const float* x = a.logits + (size_t)row * V;
+  int v0, v1;
+  row_slice(x, V, sl, S, v0, v1);
+  const Span sp(x, v0, v1);
+  // the token's logit, asked for first: at the end it would be two more waits
+  const int y = clamp_id(a.tokens[row], V);
+  const bool mine = y >= v0 && y < v1;
+  const float x_y = mine ? x[y] : 0.f;
+  const SoftPart p = span_soft<kPolThreads, ENT, ONCE>(x, sp, a.c, red);
   if (threadIdx.x == 0) {
-    stats[(size_t)row * S + sl] = p;
-    if (mine) xy[row] = x_y;
+    a.stats[(size_t)row * S + sl] = p;
+    if (mine) a.xy[row] = x_y;
   }
 }
 
@@ -303,6 +320,36 @@ __device__ __forceinline__ SoftPart row_part(const SoftPart* stats, int row, int
   return slices_soft(q < S ? stats[(size_t)row * S + q] : kNone, c);
 }
 
+struct LogpOut {
+  float logp, entropy;
+};
+
+__device__ __forceinline__ LogpOut logp_out(const SoftPart& p, float x_y, Base2 c, double inv_t) {
+  if (p.s == 0.0) return LogpOut{-INFINITY, 0.f};  // no distribution
+  const double ln_s = log(p.s);
+  return LogpOut{(float)(shift_of(x_y, p, c, inv_t) - ln_s), (float)(ln_s - 0.6931471805599453 * (p.u / p.s))};
+}
+
+// A workgroup a row, nothing to bring together.
+template <int NT, bool ENT>
+__global__ void __launch_bounds__(NT) logprobs_direct_kernel(StatsDev a, double inv_t, float* __restrict__ logp,
+                                                             float* __restrict__ entropy) {
+  __shared__ SoftPart red[NT / 64];
+  const int row = turned_row(blockIdx.x, gridDim.x);
+  LogpOut r{0.f, 0.f};
+  if (!(a.weights && a.weights[row] == 0.f)) {
+    const float* x = a.logits + (size_t)row * a.V;
+    const float x_y = x[clamp_id(a.tokens[row], a.V)];
+    const Span sp(x, 0, a.V);
+    const SoftPart p = span_soft<NT, ENT, true>(x, sp, a.c, red);
+    r = logp_out(p, x_y, a.c, inv_t);
+  }
+  if (threadIdx.x == 0) {
+    logp[row] = r.logp;
+    if (ENT) entropy[row] = r.entropy;
+  }
+}
+
 // 32 lanes a row
 __global__ void __launch_bounds__(kPolThreads)
     logprobs_rows_kernel(int rows, int S, Base2 c, double inv_t, const SoftPart* __restrict__ stats,
@@ -310,21 +357,13 @@ __global__ void __launch_bounds__(kPolThreads)
                          float* __restrict__ entropy) {
   const int row = blockIdx.x * (kPolThreads / 32) + (threadIdx.x >> 5);
   if (row >= rows) return;
-  float lp = 0.f, h = 0.f;
   const float x_y = xy[row], w = weights ? weights[row] : 1.f;
   const SoftPart p = row_part(stats, row, S, c);
-  if (w != 0.f) {
-    if (p.s == 0.0) {
-      lp = -INFINITY;
-    } else {
-      const double ln_s = log(p.s);
-      lp = (float)(shift_of(x_y, p, c, inv_t) - ln_s);
-      h = (float)(ln_s - 0.6931471805599453 * (p.u / p.s));
-    }
-  }
+  LogpOut r{0.f, 0.f};
+  if (w != 0.f) r = logp_out(p, x_y, c, inv_t);
   if ((threadIdx.x & 31) == 0) {
-    logp[row] = lp;
-    if (entropy) entropy[row] = h;
+    logp[row] = r.logp;
+    if (entropy) entropy[row] = r.entropy;
   }
 }
 
@@ -555,7 +594,7 @@ typedef __attribute__((address_space(3))) void* held_lptr_t;
 
 template <int NT, int H, int RM>
 __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
-  static_assert(H % 4 == 0 && RM % 4 == 0 && H > RM, "layers go in fours");
+  static_assert(H % 4 == 0 && RM % 4 == 0 && H >= RM, "layers go in fours");
   constexpr int WAVES = NT / 64;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   f32x4* lds = reinterpret_cast<f32x4*>(smem);  // [L][NT]
@@ -715,7 +754,7 @@ static int held_layers(int V, int NT) { return V < 8 ? 0 : ((V - 6) / 4) / NT; }
 // on a compute unit (which then reads one row while it writes another), else
 // 512; 0 threads: rows too short or too long for it.
 static int held_threads(int V) {
-  if (held_layers(V, 256) < 8 || held_layers(V, 512) > kHeldMost) return 0;
+  if (held_layers(V, 256) < 4 || held_layers(V, 512) > kHeldMost) return 0;
   return held_layers(V, 256) < 48 + kHeldLds + 8 ? 256 : 512;
 }
 static int held_rows(int rows, int V, int num_cu) {
@@ -743,7 +782,8 @@ static hipError_t launch_held_rows(const PolicyDev& d, hipStream_t s) {
   if (layers >= 36) return launch_held<256, 36, 12>(d, 0, s);
   if (layers >= 24) return launch_held<256, 24, 12>(d, 0, s);
   if (layers >= 16) return launch_held<256, 16, 8>(d, 0, s);
-  return launch_held<256, 8, 4>(d, std::min(layers - 8, 4), s);
+  if (layers >= 8) return launch_held<256, 8, 4>(d, std::min(layers - 8, 4), s);
+  return launch_held<256, 4, 4>(d, 0, s);
 }
 
 static Base2 base2_factor(double temperature) {
@@ -753,29 +793,48 @@ static Base2 base2_factor(double temperature) {
   return Base2{hi, (float)(c - (double)hi)};
 }
 
-// ONCE: the logits are not read again (non-temporal loads)
 template <bool ENT, bool ONCE>
-static void launch_stats(int row0, int rows, int V, int S, Base2 c, const float* logits, const int32_t* tokens,
-                         const float* weights, SoftPart* stats, float* xy, unsigned int* ticket, hipStream_t s) {
-  hipLaunchKernelGGL((policy_stats_kernel<ENT, ONCE>), dim3((unsigned)(rows - row0) * (unsigned)S), dim3(kPolThreads),
-                     0, s, row0, rows, V, S, c, logits, tokens, weights, stats, xy, ticket);
+static void launch_stats(const StatsDev& a, hipStream_t s) {
+  hipLaunchKernelGGL((policy_stats_kernel<ENT, ONCE>), dim3((unsigned)(a.rows - a.row0) * (unsigned)a.S),
+                     dim3(kPolThreads), 0, s, a);
+}
+
+template <int NT>
+static void launch_direct(const StatsDev& a, double inv_t, float* logp, float* entropy, hipStream_t s) {
+  if (entropy)
+    hipLaunchKernelGGL((logprobs_direct_kernel<NT, true>), dim3((unsigned)a.rows), dim3(NT), 0, s, a, inv_t, logp,
+                       entropy);
+  else
+    hipLaunchKernelGGL((logprobs_direct_kernel<NT, false>), dim3((unsigned)a.rows), dim3(NT), 0, s, a, inv_t, logp,
+                       entropy);
 }
 
 hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
                                  double temperature, float* logp, float* entropy, const PolicyPlan& plan,
-                                 void* workspace, hipStream_t s) {
+                                 void* workspace, int num_cu, hipStream_t s) {
   if (B <= 0) return hipSuccess;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  SoftPart* stats = reinterpret_cast<SoftPart*>(ws + plan.stats);
-  float* xy = reinterpret_cast<float*>(ws + plan.xy);
-  const int rows = B * K;
-  const Base2 c = base2_factor(temperature);
+  const StatsDev a{0,      B * K,  V,       plan.S, base2_factor(temperature),
+                   logits, tokens, weights, reinterpret_cast<SoftPart*>(ws + plan.stats),
+                   reinterpret_cast<float*>(ws + plan.xy), nullptr};
+  const double inv_t = 1.0 / temperature;
+  // Short rows, and longer ones of a small call, take a workgroup each and one
+  // launch: what a small call costs is its launches (16 x 20000: 8.4 us against 10.5
+  // sliced; 16 x 60000: 12.2 and 9.6 us; 512 x 32000: 23 and 16 us).  1024 threads while there are fewer
+  // rows than fill the device, so that a row is in flight at once.
+  if (V <= 8192 || (V <= 32768 && (long)a.rows * V <= 1l << 22) || plan.S == 1) {
+    if (V > 4096 && a.rows < 4 * num_cu)
+      launch_direct<1024>(a, inv_t, logp, entropy, s);
+    else
+      launch_direct<kPolThreads>(a, inv_t, logp, entropy, s);
+    return hipGetLastError();
+  }
   if (entropy)
-    launch_stats<true, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, nullptr, s);
+    launch_stats<true, true>(a, s);
   else
-    launch_stats<false, true>(0, rows, V, plan.S, c, logits, tokens, weights, stats, xy, nullptr, s);
-  hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((rows + kPolThreads / 32 - 1) / (kPolThreads / 32))),
-                     dim3(kPolThreads), 0, s, rows, plan.S, c, 1.0 / temperature, stats, xy, weights, logp, entropy);
+    launch_stats<false, true>(a, s);
+  hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((a.rows + kPolThreads / 32 - 1) / (kPolThreads / 32))),
+                     dim3(kPolThreads), 0, s, a.rows, plan.S, a.c, inv_t, a.stats, a.xy, weights, logp, entropy);
   return hipGetLastError();
 }
 
@@ -818,7 +877,9 @@ hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void*
     const hipError_t e = launch_held_rows(d, s);
     if (e != hipSuccess) return e;
   }
-  if (d.held < rows) launch_stats<false, false>(d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, d.ticket, s);
+  if (d.held < rows)
+    launch_stats<false, false>(
+        StatsDev{d.held, rows, a.V, plan.S, d.c, a.logits, a.tokens, a.weights, stats, xy, d.ticket}, s);
   const int left = rows - d.held;
   d.row_wgs = std::max(1, (left + kRowsPerWg - 1) / kRowsPerWg);
   // a gradient workgroup brings its row's slices together before it can begin: at

@@ -35,17 +35,21 @@ struct PolicyPlan {
   size_t total;  // workspace bytes
 };
 
-// About 8192 workgroups (positions that are not read leave at once, so that the
-// others must be many to spread evenly), each slice at least 2048 entries long, and at most 32
-// slices per row (one wave merges a row's partials).
+// Slices of a row: enough for about 1024 workgroups as long as each has 2048
+// entries, and, with 16384 entries each, for up to 8192 (positions that are not
+// read leave at once, so that the others must be many to spread evenly); at
+// most 32, since 32 lanes bring a row's slices together.
 inline PolicyPlan policy_plan(int B, int K, int V) {
   auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PolicyPlan p{};
   const long rows = (long)B * K;
-  long S = (8192 + rows - 1) / rows;
-  long smax = V / 2048 > 1 ? V / 2048 : 1;
-  smax = smax > 32 ? 32 : smax;
-  S = S < 1 ? 1 : S > smax ? smax : S;
+  auto slices = [&](long workgroups, long entries) {
+    const long want = (workgroups + rows - 1) / rows, most = V / entries;
+    return want < most ? want : most;
+  };
+  const long few = slices(1024, 2048), many = slices(8192, 16384);
+  long S = few > many ? few : many;
+  S = S < 1 ? 1 : S > 32 ? 32 : S;
   p.S = (int)S;
   p.stats = 0;
   p.xy = align256((size_t)rows * p.S * kPolicyPart);

@@ -145,7 +145,7 @@ def test_qwen_vocabulary(dev):
     _check_policy(dev, x, y, old, ref, adv, None)
 
 
-@pytest.mark.parametrize("V", [8200, 8300, 12001, 16390, 17000, 25001, 40003, 60001, 75000, 80003, 99001, 151936, 160001, 204802])
+@pytest.mark.parametrize("V", [4103, 5003, 8197, 8200, 8300, 12001, 16390, 17000, 25001, 40003, 60001, 75000, 80003, 99001, 151936, 160001, 204802])
 def test_rows_held_on_chip(dev, V):
     # as many rows as compute units and a few more: each held size, with and without rows left over
     import draft_block_causal_amd as D
