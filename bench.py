@@ -298,7 +298,11 @@ def next_rows(args, w) -> int:
                      written in place, then the backward through the correction head
                      and through time of the GRU (the whole head's gradients);
       verify:        sampled-draft verification on synthetic target / draft logits;
-      head_off:      base logits + base-only drafting, beside base logits + draft block."""
+      head_off:      base logits + base-only drafting, beside base logits + draft block;
+      roll_out:      the draft from an LM head in 8 bits (hidden states quantised, base
+                     logits of 8-bit integers, draft block), beside the same with base_logits;
+      policy_step:   the drafted tokens' log-probabilities and the clipped policy loss with
+                     its gradient."""
     import torch
 
     import domino_synth as S
@@ -385,6 +389,30 @@ def next_rows(args, w) -> int:
                        "head_on_blocks_per_s": B / ((t_lm2 + t_fr) * 1e-3),
                        "head_off_blocks_per_s": B / ((t_lm2 + t_bd) * 1e-3),
                        "base_draft_gb_s": bd_bytes / (t_bd * 1e-3) / 1e9}
+    wq, wsc = D.domino_quantize_rows(tensors["lm_head"])
+    (t_wq,) = timed([lambda: D.domino_quantize_rows(tensors["lm_head"], wq, wsc)])
+    hq, hsc = D.domino_quantize_rows(hidden)
+    qh = lambda: D.domino_quantize_rows(hidden, hq, hsc)  # noqa: E731
+    l8 = lambda: D.domino_base_logits_i8(hq, hsc, wq, wsc, base)  # noqa: E731
+    t_q, t_l8, t_fr8 = timed([qh, l8, fr])
+    out["roll_out"] = {"quantize_lm_head_ms": t_wq, "quantize_hidden_ms": t_q, "base_logits_i8_ms": t_l8,
+                       "draft_ms": t_fr8, "blocks_per_s": B / ((t_q + t_l8 + t_fr8) * 1e-3),
+                       "with_base_logits_blocks_per_s": B / ((t_lm2 + t_fr) * 1e-3)}
+
+    D.domino_draft_block(head, hidden, base, x_t, temperature=1.0, seed=w.philox_seed, tokens=tokens, logits=final,
+                         workspace=ws)
+    pws = torch.empty(D.domino_policy_loss_workspace_size(B, K, V), dtype=torch.uint8, device=dev)
+    logp = torch.empty((B, K), device=dev)
+    old = D.domino_token_logprobs(final, tokens) - 0.05
+    ref = D.domino_token_logprobs(base, tokens)
+    adv = torch.randn((B, K), device=dev)
+    lpf = lambda: D.domino_token_logprobs(final, tokens, logp=logp, workspace=pws)  # noqa: E731
+    pl = lambda: D.domino_policy_loss(final, tokens, old, adv, kl_coef=0.05, ref_logp=ref, loss=loss,  # noqa: E731
+                                      grad=base, workspace=pws)
+    t_lp, t_pl = timed([lpf, pl])
+    n = B * K * V * 4
+    out["policy_step"] = {"token_logprobs_ms": t_lp, "token_logprobs_gb_s": n / (t_lp * 1e-3) / 1e9,
+                          "policy_loss_ms": t_pl, "policy_loss_gb_s": 2 * n / (t_pl * 1e-3) / 1e9}
     print(json.dumps({"workload": w.name, "batch": B, "block": K, "vocab": V, "steps": args.steps, **out}),
           flush=True)
     return 0
@@ -472,7 +500,8 @@ def main() -> int:
     ap.add_argument("--next-rows", action="store_true",
                     help="instead of the benchmark, time the rows beyond the draft path at the workload's shapes: "
                          "the teacher-forced training forward with the curriculum loss and its logit gradients, "
-                         "sampled-draft verification, and head-off drafting beside the full head")
+                         "sampled-draft verification, head-off drafting beside the full head, the draft from an LM head in "
+                         "8 bits, and the policy loss on sampled drafts")
     ap.add_argument("--cold", action="store_true",
                     help="write a 512 MB buffer between steps (outside the timed events) so that every step starts "
                          "with the weights evicted from the on-die cache; value is then the mean of the per-step "

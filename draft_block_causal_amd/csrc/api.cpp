@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "kernels.h"
+#include "rollout.h"
 #include "validate.h"
 
 namespace {

@@ -16,7 +16,7 @@
 #include <atomic>
 
 #include "common.h"
-#include "kernels.h"
+#include "rollout.h"
 
 namespace domino {
 

@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include "loss_plan.h"
-#include "policy_plan.h"
 #include "psplit.h"
 #include "verify_plan.h"
 
@@ -365,22 +364,6 @@ hipError_t launch_curriculum_loss(int B, int K, int V, const float* base, const 
                                   const int32_t* targets, float lam, float gamma, float* loss, float* ce_base,
                                   float* ce_final, float* grad_base, float* grad_final, const LossPlan& plan,
                                   void* workspace, hipStream_t s);
-
-// Rows in 8 bits with one scale a row (quantize.hip); dtype 0 = f32, 1 = bf16.
-hipError_t launch_quantize_rows(int rows, int cols, int dtype, const void* x, int8_t* q, float* scale, hipStream_t s);
-
-// C[m][n] = a_scale[m] w_scale[n] sum_k A[m][k] W[n][k] (gemm_i8.hip): int8
-// operands, K % 32 == 0, rows contiguous, exact int32 sums.
-hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const int8_t* W, const float* w_scale, int N,
-                          int K, float* C, int num_cu, hipStream_t s);
-
-// Drafted-token log-probabilities and the clipped policy loss (policy.hip);
-// the workspace follows policy_plan(B, K, V).
-hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
-                                 double temperature, float* logp, float* entropy, const PolicyPlan& plan,
-                                 void* workspace, int num_cu, hipStream_t s);
-hipError_t launch_policy_loss(const PolicyArgs& a, const PolicyPlan& plan, void* workspace, int num_cu,
-                              hipStream_t s);
 
 hipError_t launch_accept_len(int B, int K, const int32_t* draft, const int32_t* target, int32_t* accept,
                              hipStream_t s);

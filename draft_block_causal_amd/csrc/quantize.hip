@@ -7,7 +7,7 @@
 // in and once out and no barrier (a 151936 x 4096 bf16 LM head: 287 us, 6.5 TB/s;
 // 339 us without non-temporal loads and stores).  Few rows take four waves each,
 // whose maxima meet in LDS: what a call of one block costs is the length of one
-// wave's work (16 x 4096: QUANT1 us against QUANT0).
+// wave's work (16 x 4096 on the device: 3.9 us against 6.2).
 //
 // Rounding: t = x * (127 / a) in float32 is off the exact quotient by less
 // than 2^-16 (|t| <= 127, two roundings of 2^-24 each), so rint(t) is the
@@ -17,7 +17,7 @@
 #include <math.h>
 
 #include "common.h"
-#include "kernels.h"
+#include "rollout.h"
 
 namespace domino {
 

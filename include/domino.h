@@ -446,7 +446,7 @@ int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab
  *             bytes, 256-byte aligned; its contents are overwritten.
  * batch in 0 ... 2^20 (0 is a no-op), block in 1 ... 1024, vocab in 1 ...
  * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).  Arithmetic: exponentials in float32, summed in float64 over
- * groups of 16 in a fixed order (repeated calls give the same bits); the
+ * groups of up to 16 in a fixed order (repeated calls give the same bits); the
  * logarithm and the differences in float64.
  */
 int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
@@ -478,7 +478,9 @@ size_t domino_token_logprobs_workspace_size(int32_t batch, int32_t block, int32_
  * ref_logp and advantages; its logp, kl and gradient are 0.  A row of which
  * every logit is -inf has no distribution: logp -inf, kl 0, no loss, gradient
  * 0.  A live position whose token has probability 0 has an infinite kl where
- * ref_logp is given; with kl_coef != 0 its gradient is not finite.
+ * ref_logp is given; with kl_coef != 0 its gradient is not finite.  A
+ * live position whose logits hold NaN or +inf makes its own logp, kl and (unless
+ * its advantage and kl_coef are 0) gradient and the loss NaN.
  *
  * logits      [batch, block, vocab] float32 (4-byte aligned)
  * tokens      [batch, block] int32; ids outside [0, vocab) are clamped

@@ -375,11 +375,11 @@ def test_empty_batch_leaves_the_loss(dev):
 
 
 def test_two_graphs_and_another_stream(dev):
-    # two captured calls with workspaces of their own, replayed in turn with eager calls and new inputs between them
+    # captured calls with workspaces of their own, replayed in turn with eager calls and new inputs between them
     import draft_block_causal_amd as D
 
     cases = []
-    for k, (B, K, V) in enumerate([(1, 16, 30011), (6, 5, 999)]):
+    for k, (B, K, V) in enumerate([(1, 16, 30011), (6, 5, 999), (40, 7, 5003)]):  # sliced, short, held on chip
         x, y, old, ref, adv, w = _make(B, K, V, 20 + k, cut=True)
         t = _dev(dev, x, y, old, ref, adv, w)
         ws = torch.empty(D.domino_policy_loss_workspace_size(B, K, V), dtype=torch.uint8, device=dev)
