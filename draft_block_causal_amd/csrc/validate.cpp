@@ -309,8 +309,8 @@ int check_logprobs_args(int32_t batch, int32_t block, int32_t vocab, const float
                         (const void*)entropy})
     if (reinterpret_cast<uintptr_t>(q) & 3u) return DOMINO_ERR_ALIGN;
   const size_t r = (size_t)batch * block * 4;
-  if (any_overlap({{logits, r * vocab}, {tokens, r}, {weights, r}, {workspace, workspace_bytes}},
-                  {{logp, r}, {entropy, r}}))
+  if (any_overlap({{logits, r * vocab}, {tokens, r}, {weights, r}},
+                  {{logp, r}, {entropy, r}, {workspace, workspace_bytes}}))
     return DOMINO_ERR_ARG;
   return check_policy_workspace(batch, block, vocab, workspace, workspace_bytes);
 }
@@ -333,8 +333,8 @@ int check_policy_args(const PolicyArgs& a, const void* workspace, size_t workspa
   // (a gradient in the logits' own buffer is the one overlap allowed)
   const bool in_place = a.grad == a.logits;
   if (any_overlap({{in_place ? nullptr : a.logits, n}, {a.tokens, r}, {a.old_logp, r}, {a.ref_logp, r},
-                   {a.advantages, r}, {a.weights, r}, {workspace, workspace_bytes}},
-                  {{a.grad, n}, {a.loss, 4}, {a.logp, r}, {a.kl, r}}))
+                   {a.advantages, r}, {a.weights, r}},
+                  {{a.grad, n}, {a.loss, 4}, {a.logp, r}, {a.kl, r}, {workspace, workspace_bytes}}))
     return DOMINO_ERR_ARG;
   return check_policy_workspace(a.B, a.K, a.V, workspace, workspace_bytes);
 }

@@ -392,7 +392,9 @@ int domino_gru_backward_workspace_size(const domino_head *head, int32_t batch, s
  * and the hidden states (a scale per token).  With a = max_k |x[r, k]|:
  *   scale[r] = a / 127,   q[r, k] = x[r, k] * 127 / a rounded to the nearest
  *   integer, ties to even (the exact quotient is rounded, not a rounded one)
- * so q lies in -127 ... 127 and x is about q * scale, off by at most scale / 2.
+ * so q lies in -127 ... 127 and x is about q * scale, off by scale / 2 at most
+ * but for the rounding of scale itself (half a step of float32, which is coarse
+ * for a scale below 2^-126).
  * A row of zeros has scale 0 and q 0.  A row that holds an infinity or NaN has
  * scale NaN and q 0: what is computed from it is NaN, and no other row's is.
  *
@@ -443,11 +445,13 @@ int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab
  * logp, entropy [batch, block] float32 (outputs); they overlap no input and
  *             not each other (else DOMINO_ERR_ARG)
  * workspace   device scratch of at least domino_token_logprobs_workspace_size()
- *             bytes, 256-byte aligned; its contents are overwritten.
+ *             bytes, 256-byte aligned; its contents are overwritten.  It
+ *             overlaps no input or output (else DOMINO_ERR_ARG).
  * batch in 0 ... 2^20 (0 is a no-op), block in 1 ... 1024, vocab in 1 ...
- * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).  Arithmetic: exponentials in float32, summed in float64 over
- * groups of up to 16 in a fixed order (repeated calls give the same bits); the
- * logarithm and the differences in float64.
+ * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).
+ * Arithmetic: exponentials in float32, summed in float64 over groups of up to
+ * 16 in a fixed order (repeated calls give the same bits); the logarithm and
+ * the differences in float64.
  */
 int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
                           const float *weights, double temperature, float *logp, float *entropy, void *workspace,
@@ -496,7 +500,8 @@ size_t domino_token_logprobs_workspace_size(int32_t batch, int32_t block, int32_
  *             be the logits' own buffer; otherwise no output overlaps an input
  *             or another output (else DOMINO_ERR_ARG).
  * workspace   device scratch of at least domino_policy_loss_workspace_size()
- *             bytes, 256-byte aligned; its contents are overwritten.
+ *             bytes, 256-byte aligned; its contents are overwritten.  It
+ *             overlaps no input or output (else DOMINO_ERR_ARG).
  * batch in 0 ... 2^20 (0 is a no-op that leaves loss untouched), block in
  * 1 ... 1024, vocab in 1 ... 2^24 - 1; batch * block <= 2^22 (else
  * DOMINO_ERR_UNSUPPORTED).  Arithmetic: as domino_token_logprobs;

@@ -133,3 +133,16 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         D.domino_policy_loss(x, y, z((2, 3)), z((2, 3)))
     with pytest.raises(TypeError):
         D.domino_quantize_rows([[1.0] * 32])
+
+
+def test_workspace_over_an_input_is_refused(lib):
+    """The workspace is written while the inputs are being read."""
+    n, r = 2 * 3 * 50 * 4, 2 * 3 * 4
+    for name, p, size in (("logits", 0x100000, n), ("tokens", 0x10000, r), ("w", 0x50000, r)):
+        assert _logp(lib, **{name: p}, ws=p) == E_ARG, name
+        assert _logp(lib, **{name: p - size}, ws=p) != E_ARG, name  # right before it
+    for name, p, size in (("logits", 0x100000, n), ("tokens", 0x20000, r), ("old", 0x60000, r), ("ref", 0x70000, r),
+                          ("adv", 0x80000, r), ("w", 0x90000, r)):
+        assert _policy(lib, **{name: p}, ws=p) == E_ARG, name
+        assert _policy(lib, **{name: p - size}, ws=p) != E_ARG, name
+    assert _policy(lib, grad=0x100000, ws=0x100000) == E_ARG  # the logits' own buffer
