@@ -23,7 +23,8 @@ namespace domino {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ i32x4 mma16_i8(i32x4 acc, u32x4 w, u32x4 a) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, a), acc, 0, 0, 0);
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, a), acc, 0, 0,
+                                               0);
 }
 
 // Allows a kernel its dynamic LDS, once a device (bit d of `done`).
@@ -136,7 +137,8 @@ __global__ void __launch_bounds__(NW * 64)
       float* c = C + (size_t)m * N + n0;
       const float* o = out + m * stride;
       if ((N & 3) == 0) {
-        for (int e = lane * 4; e < cols; e += 256) __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(o + e), reinterpret_cast<f32x4*>(c + e));
+        for (int e = lane * 4; e < cols; e += 256)
+          __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(o + e), reinterpret_cast<f32x4*>(c + e));
       } else {
         for (int e = lane; e < cols; e += 64) c[e] = o[e];
       }
@@ -245,6 +247,11 @@ static hipError_t launch_stream(const int8_t* A, const float* as, int M, const i
 // of two apart are then not all read at the same offset, that is from the same
 // memory channels, at a time (172 -> 149 us; with several M tiles, which share
 // W in the L2, 353 -> 361 us at 512 rows: not done).
+// With P = 2 a workgroup's tiles go in pairs: the first one's results are kept
+// in registers and stored with the second's, since stores between two tiles
+// hold up the second's loads (128 rows: vocabulary 151936, d = 2560 104 -> 100
+// us, d = 1024 51 -> 48; 128000, d = 2560 81 -> 70; but d = 256 25.3 -> 25.9).  256 x
+// 256 tiles have no registers left for it.
 // The two rows of waves alternate, one phase apart: one reads the fragments of
 // half a step (64 bytes of K) and issues loads while the other multiplies,
 // with a barrier between phases.  Order: the loads into a slot are issued one
@@ -258,30 +265,30 @@ typedef __attribute__((address_space(3))) void* lptr_t;
 
 __device__ const unsigned char kZeros[16] = {};  // what A reads past K
 
-template <int BM, int BN, int WS, int AS>
+template <int BM, int BN, int WS, int AS, int P>
 struct TileI8 {
   static constexpr int kThreads = 512, kBN = BN, kRow = 128;
   static constexpr int kABytes = BM * kRow, kWBytes = kBN * kRow;
   static constexpr int kRings = WS * kWBytes + AS * kABytes;
-  // scales of a tile, in LDS where there is room (two tiles' in turn)
-  static constexpr bool kScalesInLds = kRings + 2 * (BM + BN) * 4 <= 160 * 1024;
-  static constexpr int kLds = kRings + (kScalesInLds ? 2 * (BM + BN) * 4 : 0);
-  static constexpr int kStores = BM / 2 / 16 * (BN / 4 / 16);  // of a whole tile, per wave
+  // scales of a tile, in LDS where there is room (two tiles', or two pairs', in turn)
+  static constexpr bool kScalesInLds = kRings + 2 * P * (BM + BN) * 4 <= 160 * 1024;
+  static constexpr int kLds = kRings + (kScalesInLds ? 2 * P * (BM + BN) * 4 : 0);
   static constexpr int kAL = BM / 32, kWL = kBN / 32;  // loads of a step per loading wave
   static constexpr int kFA = BM / 2 / 16, kFW = kBN / 4 / 16;
-  static_assert(BM % 128 == 0 && BN % 64 == 0 && WS >= 2 && AS >= 2 && (WS - 2) * kWL < 64 && (AS - 2) * kAL < 64, "rings");
+  static_assert(BM % 128 == 0 && BN % 64 == 0 && WS >= 2 && AS >= 2 && (WS - 2) * kWL < 64 && (AS - 2) * kAL < 64,
+                "rings");
   static_assert(kLds <= 160 * 1024, "LDS");
 };
 
 // vmcnt(n), lgkmcnt(0); expcnt at its maximum
 #define DOMINO_I8_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | 0x0070)
 
-template <int BM, int BN, int WS, int AS>
+template <int BM, int BN, int WS, int AS, int P>
 __global__ void __launch_bounds__(512, 1)
     gemm_i8_tiled_kernel(const int8_t* __restrict__ A, const float* __restrict__ as, int M,
                          const int8_t* __restrict__ W, const float* __restrict__ ws, int N, int K,
                          float* __restrict__ C, int num_m, int num_n) {
-  using T = TileI8<BM, BN, WS, AS>;
+  using T = TileI8<BM, BN, WS, AS, P>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, col = lane & 15;
   const int wm = wave >> 2, wn = wave & 3;
@@ -368,8 +375,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int i = 0; i < BN / 64; ++i)
           if (i % 4 == w)
-            __builtin_amdgcn_global_load_lds((gptr_t)(ws + min(n0 + i * 64 + lane, N - 1)), (lptr_t)(dst + i * 64), 4, 0,
-                                             0);
+            __builtin_amdgcn_global_load_lds((gptr_t)(ws + min(n0 + i * 64 + lane, N - 1)), (lptr_t)(dst + i * 64), 4,
+                                             0, 0);
       } else {
 #pragma unroll
         for (int i = 0; i < BM / 64; ++i)
@@ -396,9 +403,8 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; i < T::kFA; ++i) asm volatile("" : "+v"(sm[i]));
   };
   const bool vec = (N & 3) == 0;  // then every group of 4 columns is 16-byte aligned and whole
-  // Whether every store of the tile was made: the count of loads in flight that
-  // a wave may wait for includes its stores.
-  auto store = [&](int parity) {
+  // (writes the results and clears them)
+  auto store = [&](int parity, i32x4 (&acc)[T::kFA][T::kFW], int m0, int n0) {
     if constexpr (T::kScalesInLds) {
       const float* src = lds_scales + parity * (BM + BN);
 #pragma unroll
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         c += (size_t)16 * N;
       }
-      return true;
+      return;
     }
 #pragma unroll
     for (int i = 0; i < T::kFA; ++i) {
@@ -448,7 +454,6 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
     }
-    return false;
   };
 
   seek();
@@ -461,7 +466,10 @@ __global__ void __launch_bounds__(512, 1)
 
   int d = 0, tile = 0, sa_slot = 0, sw_slot = 0;
   tile_at(0, m0, n0);
-  bool stored = false;  // the step before stored a whole tile
+  // the first tile of a pair, while the second is being multiplied
+  i32x4 kept[P == 2 ? T::kFA : 1][P == 2 ? T::kFW : 1];
+  bool have = false;
+  int km = 0, kn = 0;
   for (int g = 0; g < total; ++g) {
     const unsigned char* sW = smem + sw_slot * T::kWBytes + wn * T::kFW * 2048 + col * 128;
     const unsigned char* sA = smem + WS * T::kWBytes + sa_slot * T::kABytes + wm * T::kFA * 2048 + col * 128;
@@ -475,7 +483,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
       for (int i = 0; i < T::kFA; ++i) af[i] = ld16(sA + i * 2048 + slot);
       if (h == 0) {
-        if (d == 0) scales(tile & 1);
+        if (d == 0) scales(tile & (2 * P - 1));
         if (g + ahead < total) issue();
         if (T::kScalesInLds && nd == 1) {
           // a tile of one step: the first row of waves stores while the second is
@@ -489,19 +497,12 @@ __global__ void __launch_bounds__(512, 1)
         } else {
           __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         }
-      } else if (loads_w && g + WS - 1 < total) {
-        // (step g + 1's loads were issued before the stores where the ring is deeper than 2)
-        if (WS > 2 && T::kScalesInLds && stored)
-          DOMINO_I8_WAIT((WS - 2) * T::kWL + T::kStores);
-        else
-          DOMINO_I8_WAIT((WS - 2) * T::kWL);
-      } else if (!loads_w && g + AS - 1 < total) {
-        if (AS > 2 && T::kScalesInLds && stored)
-          DOMINO_I8_WAIT((AS - 2) * T::kAL + T::kStores);
-        else
-          DOMINO_I8_WAIT((AS - 2) * T::kAL);
-      } else {
+      } else if (g + ahead >= total) {
         DOMINO_I8_WAIT(0);
+      } else if (loads_w) {
+        DOMINO_I8_WAIT((WS - 2) * T::kWL);
+      } else {
+        DOMINO_I8_WAIT((AS - 2) * T::kAL);
       }
       if (h == 1 && d == 0) take_scales();
       __builtin_amdgcn_sched_barrier(0);
@@ -512,10 +513,25 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
         for (int j = 0; j < T::kFW; ++j) acc[i][j] = mma16_i8(acc[i][j], wf[j], af[i]);
       __builtin_amdgcn_sched_barrier(0);
-      // (a wait that leaves out the stores also leaves out the next tile's scales,
-      // which the second row of waves then has only at the end of step 1, while the
-      // first may store at the end of a tile of two)
-      if (h == 1) stored = d == nd - 1 && store(tile & 1) && nd > 2;
+      if (h == 1 && d == nd - 1) {
+        if (P == 2 && !have && tile + 1 < mine) {
+#pragma unroll
+          for (int i = 0; i < T::kFA; ++i)
+#pragma unroll
+            for (int j = 0; j < T::kFW; ++j) {
+              if constexpr (P == 2) kept[i][j] = acc[i][j];
+              acc[i][j] = i32x4{0, 0, 0, 0};
+            }
+          have = true;
+          km = m0;
+          kn = n0;
+        } else {
+          if constexpr (P == 2)
+            if (have) store((tile - 1) & 3, kept, km, kn);
+          store(tile & (2 * P - 1), acc, m0, n0);
+          have = false;
+        }
+      }
       __builtin_amdgcn_s_barrier();
     }
     if (++sa_slot == AS) sa_slot = 0;
@@ -528,19 +544,19 @@ __global__ void __launch_bounds__(512, 1)
   if (wm == 0) __builtin_amdgcn_s_barrier();  // equal barrier counts in both rows of waves
 }
 
-template <int BM, int BN, int WS, int AS>
+template <int BM, int BN, int WS, int AS, int P>
 static hipError_t launch_tiled(const int8_t* A, const float* as, int M, const int8_t* W, const float* ws, int N, int K,
                                float* C, int num_cu, hipStream_t s) {
-  using T = TileI8<BM, BN, WS, AS>;
+  using T = TileI8<BM, BN, WS, AS, P>;
   const int num_m = (M + BM - 1) / BM, num_n = (N + T::kBN - 1) / T::kBN;
   // a multiple of 8 workgroups, at most one a compute unit
   const int want = (num_n + 7) / 8 * num_m, have = std::max(1, num_cu / 8);
-  auto kern = gemm_i8_tiled_kernel<BM, BN, WS, AS>;
+  auto kern = gemm_i8_tiled_kernel<BM, BN, WS, AS, P>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(kern), T::kLds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * std::min(want, have))), dim3(T::kThreads), T::kLds, s, A, as, M, W, ws, N,
-                     K, C, num_m, num_n);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(8 * std::min(want, have))), dim3(T::kThreads), T::kLds, s, A, as, M, W, ws,
+                     N, K, C, num_m, num_n);
   return hipGetLastError();
 }
 
@@ -549,8 +565,8 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
   if (M <= 0 || N <= 0) return hipSuccess;
   if (K <= 0 || K % 32 || K > 8192) return hipErrorNotSupported;
   // Up to 64 rows W is streamed past A in registers (Qwen3-8B head, 64 rows:
-  // 118 us against 170 tiled); above, two workgroups would share each stream
-  // (128 rows: 160 us, against 149 tiled).
+  // 118 us against 170 tiled, before its tiles went in pairs); above, two
+  // workgroups would share each stream (128 rows: 160 us, against 135 tiled).
   if (M <= 64 && K <= 4096) {
     if (K <= 256) return launch_stream<4, 1>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
     if (K <= 512) return launch_stream<4, 2>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
@@ -560,13 +576,18 @@ hipError_t launch_gemm_i8(const int8_t* A, const float* a_scale, int M, const in
     return launch_stream<8, 8>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
   }
   if (M <= 16) return launch_stream_g<16, 8, 1>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
-  if (M > 128) return launch_tiled<256, 256, 2, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  if (M > 128) return launch_tiled<256, 256, 2, 3, 1>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
   // One M tile: 256 or 320 columns a tile, whichever leaves a compute unit fewer
-  // columns in all (Qwen3 vocabulary on 256 compute units: 3 rounds of 256 or 2 of
-  // 320; 128 rows, d = 2560: 113 and 105 us, d = 4096: 147 and 150 us).
+  // columns in all (vocabulary 151936 on 256 compute units: 3 rounds of 256 or 2 of
+  // 320; 128 rows, d = 1024: 53 and 48 us, 2560: 101.5 and 99.7); but 256 for long
+  // rows, unless 320 take a single round, as its deeper ring of A then counts for
+  // more (d = 3200: 117 us both; 3584: 122 and 129, 4096: 135 and 150, 5120: 186 and
+  // 181, 8192: 247 and 258; in one round, vocabulary 80000, d = 4096: 90 and 74).
   auto columns = [&](int bn) { return ((N + bn - 1) / bn + num_cu - 1) / num_cu * bn; };
-  return columns(320) < columns(256) ? launch_tiled<128, 320, 3, 2>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
-                                     : launch_tiled<128, 256, 3, 3>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
+  const int wide = columns(320);
+  return wide < columns(256) && (K <= 3200 || wide == 320)
+             ? launch_tiled<128, 320, 3, 2, 2>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s)
+             : launch_tiled<128, 256, 3, 3, 2>(A, a_scale, M, W, w_scale, N, K, C, num_cu, s);
 }
 
 }  // namespace domino

@@ -157,6 +157,16 @@ def test_base_logits_i8_over_a_whole_vocabulary(dev, B, d, V):
     assert np.all(np.abs(got - want) <= np.abs(want) * 3.001 * 2.0**-24)
 
 
+@pytest.mark.parametrize("B,d,V", [(8, 32, 128000), (5, 64, 128001), (8, 128, 128003), (8, 160, 128000),
+                                   (8, 1024, 128000), (5, 32, 170001), (8, 128, 170001), (6, 192, 170000),
+                                   (8, 416, 170002), (8, 96, 90000), (8, 3232, 70000), (6, 3264, 135001),
+                                   (8, 32, 260000), (7, 224, 262145), (8, 32, 400001), (8, 288, 330000)])
+def test_base_logits_i8_tiles_in_pairs(dev, B, d, V):
+    # whole pairs, a single tile behind them and workgroups that differ by a tile, of 256 and of 320 columns; one step
+    # of K, two and more; ragged tiles first or second in a pair
+    test_base_logits_i8_over_a_whole_vocabulary(dev, B, d, V)
+
+
 def test_scales_of_zero_nan_and_extremes(dev):
     import draft_block_causal_amd as D
 
