@@ -64,6 +64,12 @@ __device__ __forceinline__ float ref_of(float m, Base2 c) {
 // Whether a row's maximum lies where R(m) does not serve (not: no entry at all).
 __device__ __forceinline__ bool far_out(float m, Base2 c) { return m != -INFINITY && !(fabsf(m * c.hi) < kRefMax); }
 
+// What the sums of a part with maximum m are relative to: R(m), or c m where that
+// does not serve.
+__device__ __forceinline__ double base_of(float m, Base2 c) {
+  return far_out(m, c) ? (double)m * ((double)c.hi + (double)c.lo) : (double)ref_of(m, c);
+}
+
 // t relative to R
 __device__ __forceinline__ float base2(float x, float R, Base2 c) { return fmaf(x, c.lo, fmaf(x, c.hi, -R)); }
 
@@ -295,15 +301,20 @@ __global__ void __launch_bounds__(kPolThreads) policy_stats_kernel(StatsDev a) {
 }
 
 // The part of a row from its S <= 32 slices' parts, one a lane of a group of 32
-// (kNone in the other lanes); the result in every lane of the group.  (A
-// far-out slice below a maximum that is not adds nothing.)
+// (kNone in the other lanes); the result in every lane of the group.  Where one of
+// the two is far out, a slice is brought to the row's maximum by a factor that is
+// no power of two: its base and the row's are of different kinds.
 __device__ __forceinline__ SoftPart slices_soft(SoftPart p, Base2 c) {
   float m = p.m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if (!far_out(m, c)) return lanes_soft<32>(p, c);
-  const float t = p.m == -INFINITY ? -INFINITY : (p.m - m) * c.hi, e = exp2_hw(t);
-  p = SoftPart{m, e * p.s, e * (p.u + fmaxf(t, -200.f) * p.s)};
+  if (far_out(m, c) || far_out(p.m, c)) {
+    // (a slice without entries has no base; its sums are 0, or NaN)
+    const double d = p.m == -INFINITY ? 0.0 : base_of(p.m, c) - base_of(m, c), e = exp2(d);
+    p = SoftPart{m, e * p.s, e == 0.0 ? 0.0 : e * fma(d, p.s, p.u)};
+  } else {
+    p = soft_to(p, m, c);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     p.s += __shfl_xor(p.s, o);
