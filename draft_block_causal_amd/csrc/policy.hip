@@ -8,9 +8,11 @@
 // where coef is the loss's derivative with respect to logp times w / T.
 // R is an integer so that sums over different references are brought together
 // by exact factors; t_v is one fused product (and a second one for the part of
-// c below float32), so it is off by about |t_v| 2^-23 at most, and the terms that make
-// up s have |t_v| of order 1.  R is exact and t_v finite while |c M| < 2^30; a row
-// outside (a mask value in every entry, say) is taken again with t_v = c (x_v - M).
+// c below float32), so it is off by about |t_v| 2^-23 at most, and the largest terms
+// of s have |t_v| < 1: while |c M| < 2^20, the product that R is rounded from and the
+// part of c that it leaves out put R within 1/2 + 2^-4 + 2^-3 of c M.  (At 2^30 that
+// were 160, past what an exponential can hold.)  A row outside (a mask value in every
+// entry, say) is taken again with t_v = c (x_v - M).
 // What a row has one of (ln s, the ratio, the divergence, the loss) is in
 // float64: a divergence is a small difference of numbers near 10.
 //
@@ -57,7 +59,7 @@ struct SoftPart {
 
 __device__ __forceinline__ float exp2_hw(float t) { return __builtin_amdgcn_exp2f(t); }
 
-constexpr float kRefMax = 1073741824.f;  // 2^30
+constexpr float kRefMax = 1048576.f;  // 2^20
 __device__ __forceinline__ float ref_of(float m, Base2 c) {
   return fminf(fmaxf(rintf(m * c.hi), -kRefMax), kRefMax);
 }
