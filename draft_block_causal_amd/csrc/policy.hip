@@ -7,12 +7,15 @@
 //     grad_v = coef (1[v = y] - 2^t_v / s),
 // where coef is the loss's derivative with respect to logp times w / T.
 // R is an integer so that sums over different references are brought together
-// by exact factors; t_v is one fused product (and a second one for the part of
-// c below float32), so it is off by about |t_v| 2^-23 at most, and the largest terms
-// of s have |t_v| < 1: while |c M| < 2^20, the product that R is rounded from and the
-// part of c that it leaves out put R within 1/2 + 2^-4 + 2^-3 of c M.  (At 2^30 that
-// were 160, past what an exponential can hold.)  A row outside (a mask value in every
-// entry, say) is taken again with t_v = c (x_v - M).
+// by exact factors; t_v is two fused products, with the first 16 bits of c and
+// with the rest, so it is off by about |t_v| 2^-23 at most.  Their roundings have
+// no preferred direction: with all 24 bits of a float32 in the first part, the
+// second product would be below half a step of most t_v and be lost (mean error
+// of a log-probability over 151936 entries at T = 1.2: 1.6e-8, 2e-9 so).
+// While |c M| < 2^20, the two roundings before R's own put R within 1/2 + 2^-3 of
+// c M, so the largest terms of s have |t_v| < 1.  (At 2^30 they were past what an
+// exponential can hold.)  A row outside (a mask value in every entry, say) is taken
+// again with t_v = c (x_v - M).
 // What a row has one of (ln s, the ratio, the divergence, the loss) is in
 // float64: a divergence is a small difference of numbers near 10.
 //
@@ -33,6 +36,7 @@
 // 151936 entries: statistics 5.5 us, gradient 7.5 us, of which about 2 us each
 // are the launch).
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -44,7 +48,7 @@ namespace domino {
 constexpr int kPolThreads = 256;
 constexpr int kPolWaves = kPolThreads / 64;
 
-// log2(e) / T as a float32 pair with 0 < lo (so that x = -inf stays -inf)
+// log2(e) / T = hi + lo, hi of 16 bits, 2^-17 hi < lo (so that x = -inf stays -inf)
 struct Base2 {
   float hi, lo;
 };
@@ -60,11 +64,13 @@ struct SoftPart {
 __device__ __forceinline__ float exp2_hw(float t) { return __builtin_amdgcn_exp2f(t); }
 
 constexpr float kRefMax = 1048576.f;  // 2^20
+// c m, in two roundings (it grows with m)
+__device__ __forceinline__ float scaled(float m, Base2 c) { return fmaf(m, c.lo, m * c.hi); }
 __device__ __forceinline__ float ref_of(float m, Base2 c) {
-  return fminf(fmaxf(rintf(m * c.hi), -kRefMax), kRefMax);
+  return fminf(fmaxf(rintf(scaled(m, c)), -kRefMax), kRefMax);
 }
 // Whether a row's maximum lies where R(m) does not serve (not: no entry at all).
-__device__ __forceinline__ bool far_out(float m, Base2 c) { return m != -INFINITY && !(fabsf(m * c.hi) < kRefMax); }
+__device__ __forceinline__ bool far_out(float m, Base2 c) { return m != -INFINITY && !(fabsf(scaled(m, c)) < kRefMax); }
 
 // What the sums of a part with maximum m are relative to: R(m), or c m where that
 // does not serve.
@@ -184,7 +190,7 @@ template <int WAVES>
 __device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 c, SoftPart* red) {
   double s = 0.0, u = 0.0;
   for (int v = v0 + threadIdx.x; v < v1; v += WAVES * 64) {
-    const float t = (x[v] - m) * c.hi, f = exp2_hw(t);
+    const float t = (x[v] - m) * (c.hi + c.lo), f = exp2_hw(t);
     s += (double)f;
     u += (double)(f * fmaxf(t, -200.f));
   }
@@ -328,7 +334,8 @@ __device__ __forceinline__ SoftPart slices_soft(SoftPart p, Base2 c) {
 // ln of the row's sum with the part of logp before it: logp = shift(x_y) - ln s.
 __device__ __forceinline__ double shift_of(float xy, const SoftPart& p, Base2 c, double inv_t) {
   if (far_out(p.m, c)) return ((double)xy - (double)p.m) * inv_t;
-  return (double)xy * inv_t - 0.6931471805599453 * (double)ref_of(p.m, c);
+  // (with the terms' own c: R may be large)
+  return 0.6931471805599453 * fma((double)xy, (double)c.hi + (double)c.lo, -(double)ref_of(p.m, c));
 }
 
 __device__ __forceinline__ SoftPart row_part(const SoftPart* stats, int row, int S, Base2 c) {
@@ -510,7 +517,7 @@ __device__ __forceinline__ GradRow grad_row(const RowTerms& r, const SoftPart& p
 }
 
 __device__ __forceinline__ float grad_of(float x, const GradRow& g, Base2 c) {
-  const float t = g.far ? (x - g.ref) * c.hi : base2(x, g.ref, c);
+  const float t = g.far ? (x - g.ref) * (c.hi + c.lo) : base2(x, g.ref, c);
   return g.k * exp2_hw(t);
 }
 
@@ -805,8 +812,16 @@ static hipError_t launch_held_rows(const PolicyDev& d, hipStream_t s) {
 
 static Base2 base2_factor(double temperature) {
   const double c = 1.4426950408889634 / temperature;
-  float hi = (float)c;
-  if ((double)hi >= c) hi = nextafterf(hi, 0.f);
+  const float f = (float)c;
+  uint32_t bits;
+  memcpy(&bits, &f, 4);
+  bits &= ~0xFFu;
+  float hi;
+  memcpy(&hi, &bits, 4);
+  if (c - (double)hi < (double)hi * 0x1p-17) {  // leave something for lo
+    bits -= 0x100u;
+    memcpy(&hi, &bits, 4);
+  }
   return Base2{hi, (float)(c - (double)hi)};
 }
 

@@ -137,3 +137,27 @@ def test_rows_far_from_zero_at_any_temperature(dev, sign, base, T):
         # as above with rel(s) of the row; a term that weighs anything has 2.8 |t| < 200
         scale = np.abs(pol["coef"])[..., None]
         assert np.all(np.abs(g - pol["grad"]) <= scale * (2.02 * _rel_s(x64, T)[..., None] + 208 * E)), (B, V)
+
+
+@pytest.mark.parametrize("T", [1.0, 0.9, 1.2])
+def test_mean_error_of_log_probabilities(dev, T):
+    # Read from the divergence at d = 1 (e - 2 = 0.72): its rounding to float32, 3e-8 at most, stands for 1.7e-8 of a
+    # log-probability, 1e-8 rms, 6e-10 in the mean of 256 rows; roundings of terms have no direction.  What is left is the
+    # exponential's own mean error, a few hundredths of a step (1.2e-7).  A low part of log2(e) / T that gets lost in t
+    # shows as 1.2e-8 or more.
+    import draft_block_causal_amd as D
+
+    V, rows = 151936, 256
+    gen = torch.Generator(device=dev).manual_seed(V)
+    x = torch.randn((rows, 1, V), generator=gen, device=dev) * 2
+    y = torch.randint(0, V, (rows, 1), generator=gen, device=dev, dtype=torch.int32)
+    now = torch.log_softmax(x.double() / T, -1).gather(2, y.long()[..., None])[..., 0]
+    one = torch.ones((rows, 1), device=dev)
+    ref = (now + 1).float()
+    d = ref.double() - now
+    for grad in (torch.empty_like(x), None):  # rows held on chip, rows in slices
+        kl = torch.zeros((rows, 1), device=dev)
+        D.domino_policy_loss(x, y, now.float(), one, ref_logp=ref, kl=kl, grad=grad, temperature=T)
+        mean = ((kl.double() - (torch.expm1(d) - d)) / (1 - d.exp())).mean().item()
+        log(f"mean error of logp at T={T}: {mean:.2e}")
+        assert abs(mean) < 8e-9
