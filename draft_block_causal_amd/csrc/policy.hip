@@ -6,6 +6,11 @@
 //     logp = ln 2 (c x_y - R) - ln s,   entropy = ln s - ln 2 u / s,
 //     grad_v = coef (1[v = y] - 2^t_v / s),
 // where coef is the loss's derivative with respect to logp times w / T.
+// The token's own term e = 2^t_y is left out of the sums and added last: with r
+// the sum of the others, s = e + r, logp = -ln(1 + r / e) and grad_y = coef r / s
+// keep their digits where the token is nearly certain, and logp is never above 0.
+// (With e among the sums grad_y was a difference of near equals: at 1 - p = 1e-6
+// off by a fifth of itself.)
 // R is an integer so that sums over different references are brought together
 // by exact factors; t_v is two fused products, with the first 16 bits of c and
 // with the rest, so it is off by about |t_v| 2^-23 at most.  Their roundings have
@@ -53,9 +58,10 @@ struct Base2 {
   float hi, lo;
 };
 
-// Maximum of some logits (the exact one), and sums relative to R(m).  The sums
-// are in float64, added to by float32 sums of 16 terms: one term near 1 would
-// swallow the last bits of hundreds of small ones (2e-6 of a divergence).
+// Maximum of some logits (the exact one), and sums relative to R(m); the drafted
+// token's logit has no part in them.  The sums are in float64, added to by float32
+// sums of 16 terms: one term near 1 would swallow the last bits of hundreds of
+// small ones (2e-6 of a divergence).
 struct SoftPart {
   float m;
   double s, u;
@@ -165,9 +171,29 @@ struct Span {
     outer = (a4 - v0) + (v1 - b4);
   }
   __device__ __forceinline__ int outer_at(int e) const { return e < a4 - v0 ? v0 + e : b4 + e - (a4 - v0); }
+  // The layer of NT groups that entry v's group belongs to (-1: not in a whole group).
+  __device__ __forceinline__ int layer(int v, int NT) const { return v >= a4 && v < b4 ? ((v - a4) >> 2) / NT : -1; }
   // The thread of NT that handles entry v (groups are dealt out in turn).
   __device__ __forceinline__ int owner(int v, int NT) const {
     return v < a4 ? v - v0 : v < b4 ? ((v - a4) >> 2) % NT : (a4 - v0) + v - b4;
+  }
+};
+
+// The drafted token's place among the groups that a workgroup takes.
+struct Token {
+  int y, layer, thread, e;  // entry of the row; layer, thread and place in the group
+  __device__ __forceinline__ Token(const Span& sp, int y_, int NT)
+      : y(__builtin_amdgcn_readfirstlane(y_)), layer(sp.layer(y, NT)), thread(sp.owner(y, NT)), e((y - sp.a4) & 3) {}
+  // Takes it out of a thread's groups of layers first, first + 1, ... (the branch on
+  // the layer is the same for all threads).
+  template <int G>
+  __device__ __forceinline__ void leave_out(f32x4* v, int first) const {
+    const unsigned at = (unsigned)(layer - first);
+    if (at < (unsigned)G && (int)threadIdx.x == thread) {
+#pragma unroll
+      for (int i = 0; i < 4 * G; ++i)
+        if (i == (int)(4 * at) + e) v[i >> 2][i & 3] = -INFINITY;
+    }
   }
 };
 
@@ -184,13 +210,13 @@ __device__ __forceinline__ SoftPart block_soft(SoftPart p, SoftPart* red, Base2 
   return p;
 }
 
-// Sums of a far-out slice with maximum m, t = c (x - m).  Every thread of the
-// workgroup calls it (red: one entry per wave, not in use).
+// Sums of a far-out slice with maximum m, t = c (x - m), without entry y.  Every
+// thread of the workgroup calls it (red: one entry per wave, not in use).
 template <int WAVES>
-__device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 c, SoftPart* red) {
+__device__ SoftPart far_out_part(const float* x, int v0, int v1, int y, float m, Base2 c, SoftPart* red) {
   double s = 0.0, u = 0.0;
   for (int v = v0 + threadIdx.x; v < v1; v += WAVES * 64) {
-    const float t = (x[v] - m) * (c.hi + c.lo), f = exp2_hw(t);
+    const float t = v == y ? -INFINITY : (x[v] - m) * (c.hi + c.lo), f = exp2_hw(t);
     s += (double)f;
     u += (double)(f * fmaxf(t, -200.f));
   }
@@ -211,10 +237,11 @@ __device__ SoftPart far_out_part(const float* x, int v0, int v1, float m, Base2 
   return p;
 }
 
-// The part of a span of a row, taken by a workgroup of NT threads (red: one entry
-// per wave); the result in every thread.
+// The part of a span of a row without entry y (which may lie outside it), taken by
+// a workgroup of NT threads (red: one entry per wave); the result in every thread.
 template <int NT, bool ENT, bool ONCE>
-__device__ __forceinline__ SoftPart span_soft(const float* x, const Span& sp, Base2 c, SoftPart* red) {
+__device__ __forceinline__ SoftPart span_soft(const float* x, const Span& sp, int y, Base2 c, SoftPart* red) {
+  const Token tok(sp, y, NT);
   SoftPart p = kNone;
   float R = ref_of(p.m, c);
   const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
@@ -238,6 +265,7 @@ __device__ __forceinline__ SoftPart span_soft(const float* x, const Span& sp, Ba
           if (step * kStep + i * NT + (int)threadIdx.x >= sp.n4)
             d[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       }
+      tok.leave_out<U>(d, step * U);
       float f[4 * U];
 #pragma unroll
       for (int e = 0; e < 4 * U; ++e) f[e] = d[e >> 2][e & 3];
@@ -254,11 +282,12 @@ __device__ __forceinline__ SoftPart span_soft(const float* x, const Span& sp, Ba
     }
   }
   if ((int)threadIdx.x < sp.outer) {
-    const float f[1] = {x[sp.outer_at(threadIdx.x)]};
+    const int v = sp.outer_at(threadIdx.x);
+    const float f[1] = {v == tok.y ? -INFINITY : x[v]};
     soft_add<1, ENT>(p, R, f, c);
   }
   p = block_soft<NT / 64>(p, red, c);
-  if (far_out(p.m, c)) p = far_out_part<NT / 64>(x, sp.v0, sp.v1, p.m, c, red);
+  if (far_out(p.m, c)) p = far_out_part<NT / 64>(x, sp.v0, sp.v1, tok.y, p.m, c, red);
   return p;
 }
 
@@ -301,28 +330,29 @@ __global__ void __launch_bounds__(kPolThreads) policy_stats_kernel(StatsDev a) {
   const int y = clamp_id(a.tokens[row], V);
   const bool mine = y >= v0 && y < v1;
   const float x_y = mine ? x[y] : 0.f;
-  const SoftPart p = span_soft<kPolThreads, ENT, ONCE>(x, sp, a.c, red);
+  const SoftPart p = span_soft<kPolThreads, ENT, ONCE>(x, sp, y, a.c, red);
   if (threadIdx.x == 0) {
     a.stats[(size_t)row * S + sl] = p;
     if (mine) a.xy[row] = x_y;
   }
 }
 
+// p brought to m >= p.m.  Where one of the two is far out the factor is no power of
+// two: their bases are of different kinds.  (A part without entries has no base; its
+// sums are 0, or NaN.)
+__device__ __forceinline__ SoftPart part_to(SoftPart p, float m, Base2 c) {
+  if (!far_out(m, c) && !far_out(p.m, c)) return soft_to(p, m, c);
+  const double d = p.m == -INFINITY ? 0.0 : base_of(p.m, c) - base_of(m, c), e = exp2(d);
+  return SoftPart{m, e * p.s, e == 0.0 ? 0.0 : e * fma(d, p.s, p.u)};
+}
+
 // The part of a row from its S <= 32 slices' parts, one a lane of a group of 32
-// (kNone in the other lanes); the result in every lane of the group.  Where one of
-// the two is far out, a slice is brought to the row's maximum by a factor that is
-// no power of two: its base and the row's are of different kinds.
+// (kNone in the other lanes); the result in every lane of the group.
 __device__ __forceinline__ SoftPart slices_soft(SoftPart p, Base2 c) {
   float m = p.m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if (far_out(m, c) || far_out(p.m, c)) {
-    // (a slice without entries has no base; its sums are 0, or NaN)
-    const double d = p.m == -INFINITY ? 0.0 : base_of(p.m, c) - base_of(m, c), e = exp2(d);
-    p = SoftPart{m, e * p.s, e == 0.0 ? 0.0 : e * fma(d, p.s, p.u)};
-  } else {
-    p = soft_to(p, m, c);
-  }
+  p = part_to(p, m, c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     p.s += __shfl_xor(p.s, o);
@@ -331,31 +361,52 @@ __device__ __forceinline__ SoftPart slices_soft(SoftPart p, Base2 c) {
   return p;
 }
 
-// ln of the row's sum with the part of logp before it: logp = shift(x_y) - ln s.
-__device__ __forceinline__ double shift_of(float xy, const SoftPart& p, Base2 c, double inv_t) {
-  if (far_out(p.m, c)) return ((double)xy - (double)p.m) * inv_t;
-  // (with the terms' own c: R may be large)
-  return 0.6931471805599453 * fma((double)xy, (double)c.hi + (double)c.lo, -(double)ref_of(p.m, c));
-}
-
 __device__ __forceinline__ SoftPart row_part(const SoftPart* stats, int row, int S, Base2 c) {
   const int q = threadIdx.x & 31;
   return slices_soft(q < S ? stats[(size_t)row * S + q] : kNone, c);
+}
+
+// A row's sums: r of the entries but the token's, and the token's term e = 2^t.
+// (The exponential, the quotient and the token's test among the groups cost a call of
+// one block 0.5 us of 13.4, a large one nothing; asking for the first groups before
+// the token's number, or taking e beforehand relative to a base of its own, gained
+// nothing.)
+struct RowSum {
+  float m;
+  double s, r, u, t, logp;
+};
+
+__device__ __forceinline__ RowSum row_sum(SoftPart p, float x_y, Base2 c) {
+  const float m = fmaxf(p.m, x_y);
+  p = part_to(p, m, c);
+  const double c64 = (double)c.hi + (double)c.lo;  // as in the other terms: R may be large
+  const double t = far_out(m, c) ? ((double)x_y - (double)m) * c64 : fma((double)x_y, c64, -(double)ref_of(m, c));
+  const double e = exp2(t), s = p.s + e;
+  // -ln(1 + q), q = r / e, with what 1 + q rounds off put back (over 1 + q, to
+  // first order); or ln 2 t - ln s
+  const bool most = p.s < e;
+  const double q = p.s / e, a = most ? 1.0 + q : s, l = log(a);
+  const double lp = most ? fma((a - 1.0) - q, 1.0 - q, -l) : fma(0.6931471805599453, t, -l);
+  return RowSum{m, s, p.s, p.u, t, lp};
 }
 
 struct LogpOut {
   float logp, entropy;
 };
 
-__device__ __forceinline__ LogpOut logp_out(const SoftPart& p, float x_y, Base2 c, double inv_t) {
-  if (p.s == 0.0) return LogpOut{-INFINITY, 0.f};  // no distribution
-  const double ln_s = log(p.s);
-  return LogpOut{(float)(shift_of(x_y, p, c, inv_t) - ln_s), (float)(ln_s - 0.6931471805599453 * (p.u / p.s))};
+__device__ __forceinline__ LogpOut logp_out(const SoftPart& p, float x_y, Base2 c) {
+  const RowSum q = row_sum(p, x_y, c);
+  if (q.s == 0.0) return LogpOut{-INFINITY, 0.f};  // no distribution
+  // ln s - ln 2 (u + e t) / s, in which what a token near 1 has of both cancels
+  // beforehand; e is 0 below
+  const double h = q.t > -4096.0 ? fma(0.6931471805599453, fma(q.t, q.r, -q.u) / q.s, -q.logp)
+                                 : log(q.s) - 0.6931471805599453 * (q.u / q.s);
+  return LogpOut{(float)q.logp, h < 0.0 ? 0.f : (float)h};
 }
 
 // A workgroup a row, nothing to bring together.
 template <int NT, bool ENT>
-__global__ void __launch_bounds__(NT) logprobs_direct_kernel(StatsDev a, double inv_t, float* __restrict__ logp,
+__global__ void __launch_bounds__(NT) logprobs_direct_kernel(StatsDev a, float* __restrict__ logp,
                                                              float* __restrict__ entropy) {
   __shared__ SoftPart red[NT / 64];
   const int row = turned_row(blockIdx.x, gridDim.x);
@@ -364,8 +415,8 @@ __global__ void __launch_bounds__(NT) logprobs_direct_kernel(StatsDev a, double 
     const float* x = a.logits + (size_t)row * a.V;
     const float x_y = x[clamp_id(a.tokens[row], a.V)];
     const Span sp(x, 0, a.V);
-    const SoftPart p = span_soft<NT, ENT, true>(x, sp, a.c, red);
-    r = logp_out(p, x_y, a.c, inv_t);
+    const SoftPart p = span_soft<NT, ENT, true>(x, sp, clamp_id(a.tokens[row], a.V), a.c, red);
+    r = logp_out(p, x_y, a.c);
   }
   if (threadIdx.x == 0) {
     logp[row] = r.logp;
@@ -375,7 +426,7 @@ __global__ void __launch_bounds__(NT) logprobs_direct_kernel(StatsDev a, double 
 
 // 32 lanes a row
 __global__ void __launch_bounds__(kPolThreads)
-    logprobs_rows_kernel(int rows, int S, Base2 c, double inv_t, const SoftPart* __restrict__ stats,
+    logprobs_rows_kernel(int rows, int S, Base2 c, const SoftPart* __restrict__ stats,
                          const float* __restrict__ xy, const float* __restrict__ weights, float* __restrict__ logp,
                          float* __restrict__ entropy) {
   const int row = blockIdx.x * (kPolThreads / 32) + (threadIdx.x >> 5);
@@ -383,7 +434,7 @@ __global__ void __launch_bounds__(kPolThreads)
   const float x_y = xy[row], w = weights ? weights[row] : 1.f;
   const SoftPart p = row_part(stats, row, S, c);
   LogpOut r{0.f, 0.f};
-  if (w != 0.f) r = logp_out(p, x_y, c, inv_t);
+  if (w != 0.f) r = logp_out(p, x_y, c);
   if ((threadIdx.x & 31) == 0) {
     logp[row] = r.logp;
     if (entropy) entropy[row] = r.entropy;
@@ -409,6 +460,7 @@ struct PolicyDev {
 struct RowTerms {
   float logp, kl;
   double term, coef;  // weighted loss term; its derivative with respect to logp, over T
+  RowSum sum;
 };
 
 // What the loss reads of a row, loaded together.  (Rows of weight 0 are read
@@ -423,9 +475,9 @@ __device__ __forceinline__ RowIn row_in(const PolicyDev& a, int row) {
 }
 
 __device__ __forceinline__ RowTerms row_terms(const PolicyDev& a, const RowIn& in, float xy, const SoftPart& p) {
-  RowTerms r{-INFINITY, 0.f, 0.0, 0.0};
-  if (p.s == 0.0) return r;  // no distribution
-  const double lp = shift_of(xy, p, a.c, a.inv_t) - log(p.s);
+  RowTerms r{-INFINITY, 0.f, 0.0, 0.0, row_sum(p, xy, a.c)};
+  if (r.sum.s == 0.0) return r;  // no distribution
+  const double lp = r.sum.logp;
   const double w = in.w, adv = in.adv, ratio = exp(lp - in.old);
   const bool inside = adv >= 0.0 ? ratio <= a.hi : ratio >= a.lo;
   // (an advantage of 0 stays 0 whatever the ratio)
@@ -467,7 +519,7 @@ __device__ void policy_rows(const PolicyDev& a) {
     const RowIn in = row_in(a, row);
     const float xy = a.xy[row];
     const SoftPart p = row_part(a.stats, row, a.S, a.c);
-    RowTerms r{0.f, 0.f, 0.0, 0.0};
+    RowTerms r{};
     if (in.w != 0.0) r = row_terms(a, in, xy, p);
     term = r.term;
     if (lane == 0) {
@@ -505,15 +557,17 @@ __device__ void policy_rows(const PolicyDev& a) {
   }
 }
 
-// What a row's gradient is made of: grad = k 2^t (+ coef at the token).
+// What a row's gradient is made of: k 2^t, and `tok` at the token.
 struct GradRow {
-  float ref, k, coef;  // ref: R, or the maximum of a far-out row
+  float ref, k, tok;  // ref: R, or the maximum of a far-out row
   int far;
 };
 
-__device__ __forceinline__ GradRow grad_row(const RowTerms& r, const SoftPart& p, Base2 c) {
-  const bool far = far_out(p.m, c);
-  return GradRow{far ? p.m : ref_of(p.m, c), r.coef == 0.0 ? 0.f : (float)(-r.coef / p.s), (float)r.coef, far};
+__device__ __forceinline__ GradRow grad_row(const RowTerms& r, Base2 c) {
+  const bool far = far_out(r.sum.m, c);
+  if (r.coef == 0.0) return GradRow{0.f, 0.f, 0.f, far};
+  const double k = r.coef / r.sum.s;
+  return GradRow{far ? r.sum.m : ref_of(r.sum.m, c), (float)-k, (float)(k * r.sum.r), far};
 }
 
 __device__ __forceinline__ float grad_of(float x, const GradRow& g, Base2 c) {
@@ -567,11 +621,11 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
   if (threadIdx.x < 32) {
     const SoftPart p = row_part(a.stats, row, a.S, a.c);
     const RowTerms r = row_terms(a, in, xy, p);
-    if (threadIdx.x == 0) sh = grad_row(r, p, a.c);
+    if (threadIdx.x == 0) sh = grad_row(r, a.c);
   }
   __syncthreads();
   const GradRow gr = sh;
-  if (gr.k == 0.f && gr.coef == 0.f) {  // no gradient here
+  if (gr.k == 0.f && gr.tok == 0.f) {  // no gradient here
     zero_span<kPolThreads>(g, sp);
     return;
   }
@@ -589,11 +643,10 @@ __global__ void __launch_bounds__(kPolThreads) policy_grad_kernel(PolicyDev a) {
       g[v] = grad_of(x[v], gr, a.c);
     }
     // (the owner's second store to the entry, in its program order)
-    if (y >= v0 && y < v1 && (int)threadIdx.x == sp.owner(y, kPolThreads)) g[y] = grad_of(xy, gr, a.c) + gr.coef;
+    if (y >= v0 && y < v1 && (int)threadIdx.x == sp.owner(y, kPolThreads)) g[y] = gr.tok;
   } else {
     for (int v = v0 + threadIdx.x; v < v1; v += kPolThreads) {
-      const float e = grad_of(x[v], gr, a.c);
-      g[v] = v == y ? e + gr.coef : e;
+      g[v] = v == y ? gr.tok : grad_of(x[v], gr, a.c);
     }
   }
 }
@@ -640,11 +693,14 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
   }
   const int y = clamp_id(a.tokens[row], a.V);
   const float xy = x[y];
+  const Token tok(sp, y, NT);
   const f32x4* x4 = reinterpret_cast<const f32x4*>(x + sp.a4);
   const int rest = (H + L) * NT;  // the first group that is not held
   SoftPart p = kNone;
   float R = ref_of(p.m, a.c);
-  auto add4 = [&](const f32x4* v) {
+  // (the token is taken out of the registers for good: its gradient comes last)
+  auto add4 = [&](f32x4* v, int layer) {
+    tok.leave_out<4>(v, layer);
     float f[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) f[e] = v[e >> 2][e & 3];
@@ -672,6 +728,7 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
     for (int i = 0; i < RM; ++i)
       if (rest + i * NT < sp.n4) {
         const bool in = rest + i * NT + tid < sp.n4;
+        tok.leave_out<1>(r + i, H + L + i);
         const float f[4] = {in ? r[i][0] : -INFINITY, in ? r[i][1] : -INFINITY, in ? r[i][2] : -INFINITY,
                             in ? r[i][3] : -INFINITY};
         soft_add<4, false>(p, R, f, a.c);
@@ -682,17 +739,18 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
   for (int i = H - RM; i < H; ++i) h[i] = __builtin_nontemporal_load(x4 + i * NT + tid);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < H; i += 4) add4(h + i);
+  for (int i = 0; i < H; i += 4) add4(h + i, i);
   if (L > 0) {
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's groups are in LDS, which only it reads
     __builtin_amdgcn_sched_barrier(0);
     int l = 0;
     for (; l + 4 <= L; l += 4) {
-      const f32x4 v[4] = {lds[l * NT + tid], lds[(l + 1) * NT + tid], lds[(l + 2) * NT + tid], lds[(l + 3) * NT + tid]};
-      add4(v);
+      f32x4 v[4] = {lds[l * NT + tid], lds[(l + 1) * NT + tid], lds[(l + 2) * NT + tid], lds[(l + 3) * NT + tid]};
+      add4(v, H + l);
     }
     for (; l < L; ++l) {
-      const f32x4 v = lds[l * NT + tid];
+      f32x4 v = lds[l * NT + tid];
+      tok.leave_out<1>(&v, H + l);
       const float f[4] = {v[0], v[1], v[2], v[3]};
       soft_add<4, false>(p, R, f, a.c);
     }
@@ -704,26 +762,27 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (at + i * NT + tid >= sp.n4) v[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    add4(v);
+    add4(v, at / NT);
   }
   if (tid < sp.outer) {
-    const float f[1] = {x[sp.outer_at(tid)]};
+    const int v = sp.outer_at(tid);
+    const float f[1] = {v == y ? -INFINITY : x[v]};
     soft_add<1, false>(p, R, f, a.c);
   }
   p = block_soft<WAVES>(p, red, a.c);
-  if (far_out(p.m, a.c)) p = far_out_part<WAVES>(x, 0, a.V, p.m, a.c, red);
+  if (far_out(p.m, a.c)) p = far_out_part<WAVES>(x, 0, a.V, y, p.m, a.c, red);
   if (tid < 64) {
     const RowTerms r = row_terms(a, in, xy, p);
     if (tid == 0) {
       if (a.logp) a.logp[row] = r.logp;
       if (a.kl) a.kl[row] = r.kl;
       a.terms[row] = r.term;
-      sh = grad_row(r, p, a.c);
+      sh = grad_row(r, a.c);
     }
   }
   __syncthreads();
   const GradRow gr = sh;
-  if (gr.k == 0.f && gr.coef == 0.f) {
+  if (gr.k == 0.f && gr.tok == 0.f) {
     zero_span<NT>(g, sp);
     return;
   }
@@ -756,7 +815,7 @@ __global__ void __launch_bounds__(NT) policy_held_kernel(PolicyDev a, int L) {
     const int v = sp.outer_at(tid);
     g[v] = grad_of(x[v], gr, a.c);
   }
-  if (tid == sp.owner(y, NT)) g[y] = grad_of(xy, gr, a.c) + gr.coef;
+  if (tid == tok.thread) g[y] = gr.tok;
 }
 
 template <int NT, int H, int RM>
@@ -832,13 +891,11 @@ static void launch_stats(const StatsDev& a, hipStream_t s) {
 }
 
 template <int NT>
-static void launch_direct(const StatsDev& a, double inv_t, float* logp, float* entropy, hipStream_t s) {
+static void launch_direct(const StatsDev& a, float* logp, float* entropy, hipStream_t s) {
   if (entropy)
-    hipLaunchKernelGGL((logprobs_direct_kernel<NT, true>), dim3((unsigned)a.rows), dim3(NT), 0, s, a, inv_t, logp,
-                       entropy);
+    hipLaunchKernelGGL((logprobs_direct_kernel<NT, true>), dim3((unsigned)a.rows), dim3(NT), 0, s, a, logp, entropy);
   else
-    hipLaunchKernelGGL((logprobs_direct_kernel<NT, false>), dim3((unsigned)a.rows), dim3(NT), 0, s, a, inv_t, logp,
-                       entropy);
+    hipLaunchKernelGGL((logprobs_direct_kernel<NT, false>), dim3((unsigned)a.rows), dim3(NT), 0, s, a, logp, entropy);
 }
 
 hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const int32_t* tokens, const float* weights,
@@ -849,16 +906,15 @@ hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const
   const StatsDev a{0,      B * K,  V,       plan.S, base2_factor(temperature),
                    logits, tokens, weights, reinterpret_cast<SoftPart*>(ws + plan.stats),
                    reinterpret_cast<float*>(ws + plan.xy), nullptr};
-  const double inv_t = 1.0 / temperature;
   // Short rows, and longer ones of a small call, take a workgroup each and one
   // launch: what a small call costs is its launches (16 x 20000: 8.4 us against 10.5
   // sliced; 16 x 60000: 12.2 and 9.6 us; 512 x 32000: 23 and 16 us).  1024 threads while there are fewer
   // rows than fill the device, so that a row is in flight at once.
   if (V <= 8192 || (V <= 32768 && (long)a.rows * V <= 1l << 22) || plan.S == 1) {
     if (V > 4096 && a.rows < 4 * num_cu)
-      launch_direct<1024>(a, inv_t, logp, entropy, s);
+      launch_direct<1024>(a, logp, entropy, s);
     else
-      launch_direct<kPolThreads>(a, inv_t, logp, entropy, s);
+      launch_direct<kPolThreads>(a, logp, entropy, s);
     return hipGetLastError();
   }
   if (entropy)
@@ -866,7 +922,7 @@ hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const
   else
     launch_stats<false, true>(a, s);
   hipLaunchKernelGGL(logprobs_rows_kernel, dim3((unsigned)((a.rows + kPolThreads / 32 - 1) / (kPolThreads / 32))),
-                     dim3(kPolThreads), 0, s, a.rows, plan.S, a.c, inv_t, a.stats, a.xy, weights, logp, entropy);
+                     dim3(kPolThreads), 0, s, a.rows, plan.S, a.c, a.stats, a.xy, weights, logp, entropy);
   return hipGetLastError();
 }
 

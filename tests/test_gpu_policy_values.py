@@ -161,3 +161,81 @@ def test_mean_error_of_log_probabilities(dev, T):
         mean = ((kl.double() - (torch.expm1(d) - d)) / (1 - d.exp())).mean().item()
         log(f"mean error of logp at T={T}: {mean:.2e}")
         assert abs(mean) < 8e-9
+
+
+@pytest.mark.parametrize("T", [1.0, 0.7])
+@pytest.mark.parametrize("B,K,V,shift", [(1, 4, 5003, 0), (1, 4, 40003, 0), (3, 5, 99, 0), (3, 5, 4099, 1), (34, 4, 5003, 0),
+                                         (34, 4, 20011, 0), (34, 4, 60001, 0), (34, 4, 151936, 0), (1, 3, 1, 0)])
+def test_nearly_certain_tokens(dev, B, K, V, shift, T):
+    # tokens of probability 1 - 1e-2 ... 1 - 1e-16 at any place of the row, in slices, short and held rows; shift: gradient
+    # rows of another alignment than the logits'.  With r the sum of the other terms over the token's, logp = -ln(1 + r),
+    # its gradient is coef r / (1 + r) and the entropy ln(1 + r) + sum p (z_y - z): all as exact as r is.
+    import draft_block_causal_amd as D
+
+    log(f"nearly certain tokens B={B} K={K} V={V} T={T}")
+    rng = np.random.default_rng(V + B)
+    x = (rng.normal(size=(B, K, V)) * 2).astype(np.float32)
+    y = rng.integers(0, V, size=(B, K)).astype(np.int32)
+    y.flat[0], y.flat[-1], y.flat[1] = 0, V - 1, max(0, V - 2)
+    gap = np.float32(T) * (rng.uniform(4, 38, size=(B, K)) + np.log(V)).astype(np.float32) + x.max(-1)
+    np.put_along_axis(x, y[..., None].astype(np.int64), gap[..., None], -1)
+    adv = rng.choice([-1.0, 0.5, 2.0], size=(B, K)).astype(np.float32)
+    z = (x.astype(np.float64) - gap[..., None]) / T
+    q = np.exp(z)
+    np.put_along_axis(q, y[..., None].astype(np.int64), 0.0, -1)
+    r = q.sum(-1)
+    lp, s = -np.log1p(r), 1 + r
+    old = (lp - rng.uniform(-0.1, 0.1, size=lp.shape)).astype(np.float32)
+    t = LOG2E * -z + 1
+    mean_t = (q * t).sum(-1) / np.maximum(r, 1e-300)
+    rel = (2.8 * mean_t + 8) * E  # of r
+    tx, ty, told, tadv = [torch.from_numpy(a).to(dev) for a in (x, y, old, adv)]
+    h = torch.full((B, K), 99.0, device=dev)
+    got = D.domino_token_logprobs(tx, ty, T, entropy=h).cpu().numpy().astype(np.float64)
+    room = np.abs(lp) * (rel + 1.01 * E) + 2.0**-149
+    assert np.all(got <= 0) and np.all(np.abs(got - lp) <= room), np.abs(got / lp - 1).max()
+    ent = np.log1p(r) - (q * z).sum(-1) / s
+    spread = (q * t * (2.8 * t + 13)).sum(-1) * E  # a term's error, its product with t, sixteen added in float32
+    got = h.cpu().numpy()
+    assert np.all(got >= 0) and np.all(np.abs(got - ent) <= spread + np.abs(lp) * rel + ent * 1.01 * E + 2.0**-149)
+    buf = torch.full((x.size + 8,), 5.5, device=dev)
+    g = buf[shift:shift + x.size].view(x.shape)
+    lpo = torch.full((B, K), 99.0, device=dev)
+    D.domino_policy_loss(tx, ty, told, tadv, temperature=T, logp=lpo, grad=g)
+    got = lpo.cpu().numpy().astype(np.float64)
+    assert np.all(got <= 0) and np.all(np.abs(got - lp) <= room)
+    ratio = np.exp(lp - old)  # inside the clip range
+    coef = -ratio * adv / (B * K) / T
+    want = coef[..., None] * (-q / s[..., None])
+    np.put_along_axis(want, y[..., None].astype(np.int64), (coef * r / s)[..., None], -1)
+    dcoef = np.abs(coef) * 1.01 * np.abs(lp) * rel
+    # the others: the term (2.8 |t| + 2), k and the product; the token: r / s and one rounding
+    term = np.abs(want) * ((2.8 * t + 8) * E + (r * rel / s + np.abs(lp) * rel * 1.01)[..., None])
+    tok = np.abs(coef) * r / s * (rel + 1.01 * E) + dcoef * r / s
+    np.put_along_axis(term, y[..., None].astype(np.int64), tok[..., None], -1)
+    err = np.abs(g.cpu().numpy() - want)
+    bad = err > term + 1e-36
+    assert not bad.any(), (np.argwhere(bad)[:3], err[bad][:3], want[bad][:3])
+    assert torch.all(buf[:shift] == 5.5) and torch.all(buf[shift + x.size:] == 5.5)
+
+
+def test_no_log_probability_above_zero(dev):
+    # rows in which nothing but the token's own term has weight: however that rounds, p is 1 and not more
+    import draft_block_causal_amd as D
+
+    rng = np.random.default_rng(5)
+    for B, V in ((64, 33), (64, 5003), (1, 40003)):
+        x = np.full((B, 16, V), -200, np.float32)
+        y = rng.integers(0, V, size=(B, 16)).astype(np.int32)
+        np.put_along_axis(x, y[..., None].astype(np.int64), rng.uniform(-30, 30, (B, 16, 1)).astype(np.float32), -1)
+        tx, ty = torch.from_numpy(x).to(dev), torch.from_numpy(y).to(dev)
+        h, lp = torch.full((B, 16), 99.0, device=dev), torch.full((B, 16), 99.0, device=dev)
+        got = D.domino_token_logprobs(tx, ty, 0.9, entropy=h)
+        assert not got.any() and not h.any(), (got.max(), h.min())
+        g = torch.full_like(tx, 99.0)
+        zero = torch.zeros((B, 16), device=dev)
+        D.domino_policy_loss(tx, ty, zero, zero + 1, temperature=0.9, logp=lp, grad=g)
+        assert not lp.any() and g.abs().max().item() < 1e-36
+        other = (ty + 1) % V  # a token of no weight beside one of all
+        D.domino_token_logprobs(tx, other, 0.9, entropy=h)
+        assert (h >= 0).all() and h.max().item() < 1e-6
