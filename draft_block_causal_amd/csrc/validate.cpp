@@ -263,11 +263,8 @@ int check_base_i8_args(int32_t batch, int32_t block, int32_t d, int32_t vocab, c
   return DOMINO_OK;
 }
 
-// (the kernels hold log2(e) / T in float32)
-static bool bad_temperature(double t) {
-  return !(t > 0.0) || !std::isfinite(t) || !std::isfinite((float)(1.4426950408889634 / t)) ||
-         (float)(1.4426950408889634 / t) < 1e-20f;
-}
+// (the kernels hold log2(e) / T as a pair of normal float32 numbers)
+static bool bad_temperature(double t) { return !(t > 2e-38 && t < 1e20); }
 
 static bool policy_shape(int32_t batch, int32_t block, int32_t vocab) {
   return batch >= 0 && batch <= kMaxPolicyBatch && block >= 1 && block <= kMaxPolicyBlock && vocab >= 1 &&

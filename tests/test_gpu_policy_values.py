@@ -239,3 +239,27 @@ def test_no_log_probability_above_zero(dev):
         other = (ty + 1) % V  # a token of no weight beside one of all
         D.domino_token_logprobs(tx, other, 0.9, entropy=h)
         assert (h >= 0).all() and h.max().item() < 1e-6
+
+
+@pytest.mark.parametrize("T", [2.1e-38, 1e-30, 1e-6, 1e6, 9.9e19])
+def test_extreme_temperatures(dev, T):
+    import draft_block_causal_amd as D
+
+    rng = np.random.default_rng(3)
+    for V in (5003, 40003):
+        x = rng.normal(size=(1, 4, V)).astype(np.float32) * 3
+        x[0, 1] = np.round(x[0, 1])  # several largest entries
+        x[0, 2, ::3] = -np.inf
+        x[0, 3, 7] = np.finfo(np.float32).min
+        y = np.argmax(x, -1).astype(np.int32)
+        y[0, 3] = 8
+        h = torch.full((1, 4), 99.0, device=dev)
+        got = D.domino_token_logprobs(torch.from_numpy(x).to(dev), torch.from_numpy(y).to(dev), T, entropy=h)
+        want, ent = O.token_logprobs(x, y, T)
+        x64 = x.astype(np.float64)
+        room = _rel_s(x64, T) + np.abs(want) * 1.01 * E
+        got = got.cpu().numpy()
+        with np.errstate(over="ignore"):  # a value past float32's largest, 3.4e38, rounds to -inf
+            same = got == want.astype(np.float32)
+        assert np.all(same | (np.abs(got - want) <= room)), (V, got, want)
+        assert np.all(np.abs(h.cpu().numpy() - ent) <= _entropy_room(x64, T, ent)), (V, h, ent)
