@@ -511,7 +511,12 @@ def _gpu_index(t: torch.Tensor, name: str) -> int:
     return t.get_device()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _public_raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of a device's current stream; a torch without GPU support, or another one, need not have the short way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
 
 def _elsewhere(index: int, stream) -> bool:
