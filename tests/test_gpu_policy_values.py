@@ -263,3 +263,87 @@ def test_extreme_temperatures(dev, T):
             same = got == want.astype(np.float32)
         assert np.all(same | (np.abs(got - want) <= room)), (V, got, want)
         assert np.all(np.abs(h.cpu().numpy() - ent) <= _entropy_room(x64, T, ent)), (V, h, ent)
+
+
+@pytest.mark.parametrize("V,extra", [(5003, 13), (20011, 0), (60001, 13), (99001, 13), (151936, 13), (151936, 0),
+                                     (151936, 140)])
+@pytest.mark.parametrize("kl_coef,T", [(0.05, 1.0), (0.0, 0.7)])
+def test_loss_and_divergence_of_held_rows(dev, V, extra, kl_coef, T):
+    # as many rows as compute units and `extra` (rows beyond a round of long ones go in slices; 140 are held again); ratios
+    # on both sides of both limits, either sign of advantage, rows of weight 0.  A ratio and the loss move with rel(s) as
+    # the log-probability does.
+    import draft_block_causal_amd as D
+
+    rows = torch.cuda.get_device_properties(dev).multi_processor_count + extra
+    log(f"held rows: V={V} rows={rows} kl_coef={kl_coef} T={T}")
+    gen = torch.Generator(device=dev).manual_seed(V + extra)
+    x = torch.randn((rows, V), generator=gen, device=dev) * 2
+    y = torch.randint(0, V, (rows, 1), generator=gen, device=dev)
+    x.scatter_add_(1, y, torch.full((rows, 1), 7.0, device=dev))
+    z = (x.double() - x.double().amax(1, keepdim=True)) / T
+    lp = z - z.exp().sum(1, keepdim=True).log()
+    p = lp.exp()
+    delta = (2.8 * LOG2E * -(p * z).sum(1) + 8) * E
+    now, p_y = lp.gather(1, y)[:, 0], p.gather(1, y)[:, 0]
+    i = torch.arange(rows, device=dev)
+    off = torch.tensor([-0.5, -0.1, 0.1, 0.22, 0.4], device=dev)[i % 5]  # ratios 0.61, 0.90, 1.11, 1.25, 1.49
+    adv = torch.randn(rows, generator=gen, device=dev) * torch.where(i // 5 % 2 == 0, 1.0, -1.0)
+    w = (torch.rand(rows, generator=gen, device=dev) + 0.5) / rows * (i % 7 != 6)
+    old, ref = (now - off).float(), (now + torch.randn(rows, generator=gen, device=dev) * 0.4).float()
+    v = lambda t: t.view(rows, 1)  # noqa: E731
+    out = {k: torch.full((rows, 1), 99.0, device=dev) for k in ("logp", "kl")}
+    grad = torch.full((rows, 1, V), 99.0, device=dev)
+    loss = D.domino_policy_loss(x.view(rows, 1, V), v(y.int()), v(old), v(adv), clip_low=0.2, clip_high=0.28, kl_coef=kl_coef,
+                                ref_logp=v(ref), weights=v(w), temperature=T, grad=grad, **out)
+    live, A, W = w != 0, adv.double(), w.double()
+    r, d = (now - old.double()).exp(), ref.double() - now
+    kl = torch.expm1(d) - d
+    plain, clipped = r * A, r.clamp(0.8, 1.28) * A
+    inside = plain <= clipped
+    assert inside[live].any() and (~inside)[live].any()
+    want = (W * (kl_coef * kl - torch.minimum(plain, clipped))).sum()
+    slope = torch.where(inside, plain.abs(), 0)
+    room = (W * (slope + kl_coef * torch.expm1(d).abs()) * 1.01 * delta).sum() + want.abs() * 1.01 * E
+    assert abs(loss.item() - want.item()) <= room.item(), (loss.item(), want.item(), room.item())
+    got = out["logp"][:, 0].double()
+    assert not got[~live].any() and ((got - now).abs() <= delta + now.abs() * 1.01 * E)[live].all()
+    got = out["kl"][:, 0].double()
+    room = torch.expm1(d).abs() * 1.01 * delta + delta**2 + kl * 1.01 * E
+    assert not got[~live].any() and ((got - kl).abs() <= room)[live].all(), (got - kl).abs().max()
+    coef = W / T * (-kl_coef * torch.expm1(d) - torch.where(inside, plain, 0))
+    dcoef = W / T * (slope + kl_coef * d.exp()) * 1.01 * delta
+    # others: the term, s, k and a product; the token: coef r / s, r of the other entries alone
+    room = p * (coef.abs()[:, None] * ((5.6 + 2.8 * LOG2E * -z) * E + delta[:, None]) + dcoef[:, None])
+    at_y = (1 - p_y) * (coef.abs() * (delta / (1 - p_y) + 1.01 * E) + dcoef)
+    room.scatter_(1, y, at_y[:, None])
+    want = -coef[:, None] * p
+    want.scatter_(1, y, (coef * (1 - p_y))[:, None])
+    bad = (grad[:, 0].double() - want).abs() > room + 1e-36
+    assert not bad.any(), (torch.nonzero(bad)[:3], bad.sum())
+
+
+def test_token_of_no_probability_in_held_rows(dev):
+    # a token whose logit is -inf has an infinite divergence, which counts only with a coefficient; the other rows are as
+    # they were
+    import draft_block_causal_amd as D
+
+    for V, extra in ((5003, 0), (99001, 13)):
+        rows = torch.cuda.get_device_properties(dev).multi_processor_count + extra
+        gen = torch.Generator(device=dev).manual_seed(V)
+        x = torch.randn((rows, 1, V), generator=gen, device=dev)
+        y = torch.randint(0, V, (rows, 1), generator=gen, device=dev, dtype=torch.int32)
+        lp = D.domino_token_logprobs(x, y)
+        one = torch.ones((rows, 1), device=dev)
+        kl, g = torch.empty_like(one), torch.empty_like(x)
+        a = D.domino_policy_loss(x, y, lp, one, ref_logp=lp, kl=kl, grad=g)
+        kl0, g0, hit = kl.clone(), g.clone(), torch.zeros(rows, dtype=torch.bool, device=dev)
+        for i in (2, rows - 1):
+            x[i, 0, y[i, 0].item()] = -np.inf
+            hit[i] = True
+        b = D.domino_policy_loss(x, y, lp, one, ref_logp=lp, kl=kl, grad=g)
+        assert (kl[hit] == np.inf).all() and not g[hit].any()  # ratio 0: neither loss nor gradient
+        assert torch.equal(kl[~hit], kl0[~hit]) and torch.equal(g[~hit], g0[~hit])
+        # each row gives -ratio / rows, ratio within rel(s) of 1; normal logits have M < 5.5 and a weighted mean of 1, so
+        # tbar < 6.5 and rel(s) < 27 e; both losses, near -1, are rounded once
+        assert abs((b - a).item() - 2 / rows) <= 2 / rows * 27 * E + 2 * E
+        assert D.domino_policy_loss(x, y, lp, one, ref_logp=lp, kl_coef=0.1, grad=g).item() == np.inf
