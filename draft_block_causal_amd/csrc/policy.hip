@@ -38,7 +38,7 @@
 //   logprobs_direct_kernel, a workgroup per row, alone: small calls, short rows.
 // Bound by HBM: a row's logits once in and its gradient once out (held), or
 // twice in and once out; a call of one block by its two launches (16 rows of
-// 151936 entries: statistics 5.5 us, gradient 7.5 us, of which about 2 us each
+// 151936 entries: statistics 5.5 us, gradient 8.2 us, of which about 2 us each
 // are the launch).
 #include <math.h>
 #include <string.h>
@@ -416,7 +416,9 @@ __global__ void __launch_bounds__(NT) logprobs_direct_kernel(StatsDev a, float* 
     const float x_y = x[clamp_id(a.tokens[row], a.V)];
     const Span sp(x, 0, a.V);
     const SoftPart p = span_soft<NT, ENT, true>(x, sp, clamp_id(a.tokens[row], a.V), a.c, red);
-    r = logp_out(p, x_y, a.c);
+    // (all waves at the same float64 chain hold each other up: 256 rows of 5003
+    // entries 9.4 us, 8.0 so)
+    if (threadIdx.x < 64) r = logp_out(p, x_y, a.c);
   }
   if (threadIdx.x == 0) {
     logp[row] = r.logp;
@@ -842,12 +844,12 @@ static int held_threads(int V) {
 }
 static int held_rows(int rows, int V, int num_cu) {
   const int nt = held_threads(V);
-  // (20000 entries: 128 rows held 11.4 us, sliced 13.5; 10000 entries, 64 rows: 11 us both)
+  // (20000 entries: 128 rows held 12.0 us, sliced 14.3; 10000 entries, 64 rows: 10 us both)
   if (nt == 256) return rows >= num_cu / 2 ? rows : 0;
   if (nt == 512) {
     // one row a compute unit: whole rounds, and a last one that is half full
-    // (151936 entries: 128 rows held 39 us, sliced 45; 400 rows 99 and 112 us; 320
-    // rows held 90 us, 84 with the last 64 sliced)
+    // (151936 entries: 128 rows held 40 us, sliced 46; 400 rows with the last 144 held
+    // 99 us, sliced 115; 320 rows held 90 us, 85 with the last 64 sliced)
     const int rest = rows % num_cu;
     return 2 * rest >= num_cu ? rows : rows - rest;
   }
@@ -907,9 +909,10 @@ hipError_t launch_token_logprobs(int B, int K, int V, const float* logits, const
                    logits, tokens, weights, reinterpret_cast<SoftPart*>(ws + plan.stats),
                    reinterpret_cast<float*>(ws + plan.xy), nullptr};
   // Short rows, and longer ones of a small call, take a workgroup each and one
-  // launch: what a small call costs is its launches (16 x 20000: 8.4 us against 10.5
-  // sliced; 16 x 60000: 12.2 and 9.6 us; 512 x 32000: 23 and 16 us).  1024 threads while there are fewer
-  // rows than fill the device, so that a row is in flight at once.
+  // launch: what a small call from a program costs is its launches (16 x 20000: 8.0
+  // us against 8.7 to 9.6 sliced, though 8.5 and 6.9 replayed from a graph; 16 x 60000:
+  // 11 and 9 us; 512 x 32000: 20.5 and 16.5 us).  1024 threads while there are fewer rows
+  // than fill the device, so that a row is in flight at once.
   if (V <= 8192 || (V <= 32768 && (long)a.rows * V <= 1l << 22) || plan.S == 1) {
     if (V > 4096 && a.rows < 4 * num_cu)
       launch_direct<1024>(a, logp, entropy, s);
