@@ -4,8 +4,9 @@
 // One wave per row: the row is read once into registers (at most 16 chunks of
 // 8 values a lane), its maximum found with lane shuffles, and the 8-byte
 // groups of q written from the same registers, so a row costs its bytes once
-// in and once out and no barrier (a 151936 x 4096 bf16 LM head: 287 us, 6.5 TB/s;
-// 339 us without non-temporal loads and stores).  Few rows take four waves each,
+// in and once out and no barrier (a 151936 x 4096 bf16 LM head: 288 to 299 us,
+// 6.2 to 6.5 TB/s, among other calls, up to 343 us back to back; 339 us without
+// non-temporal loads and stores where it took 287 with).  Few rows take four waves each,
 // whose maxima meet in LDS: what a call of one block costs is the length of one
 // wave's work (16 x 4096 on the device: 3.9 us against 6.2).
 //

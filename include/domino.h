@@ -441,7 +441,9 @@ int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab
  * logits      [batch, block, vocab] float32 (4-byte aligned)
  * tokens      [batch, block] int32; ids outside [0, vocab) are clamped
  * weights     [batch, block] float32, or NULL: every position counts
- * temperature T > 0, 2e-38 < T < 1e20 (else DOMINO_ERR_ARG)
+ * temperature 2e-38 < T < 1e20 (else DOMINO_ERR_ARG).  domino_draft_block
+ *             samples at a float32 T: to score the very distribution it drew
+ *             from, pass that rounded value
  * logp, entropy [batch, block] float32 (outputs); they overlap no input and
  *             not each other (else DOMINO_ERR_ARG)
  * workspace   device scratch of at least domino_token_logprobs_workspace_size()
@@ -450,8 +452,10 @@ int domino_base_logits_i8(int32_t batch, int32_t block, int32_t d, int32_t vocab
  * batch in 0 ... 2^20 (0 is a no-op), block in 1 ... 1024, vocab in 1 ...
  * 2^24 - 1; batch * block <= 2^22 (else DOMINO_ERR_UNSUPPORTED).
  * Arithmetic: exponentials in float32, summed in float64 over groups of up to
- * 16 in a fixed order (repeated calls give the same bits); the logarithm and
- * the differences in float64.
+ * 16 in a fixed order (repeated calls give the same bits), the token's own term
+ * apart; the logarithm and the differences in float64.  So logp is as exact as
+ * the sum of the other terms also where the token is nearly certain; logp is
+ * never above 0 nor entropy below.
  */
 int domino_token_logprobs(int32_t batch, int32_t block, int32_t vocab, const float *logits, const int32_t *tokens,
                           const float *weights, double temperature, float *logp, float *entropy, void *workspace,
@@ -478,13 +482,15 @@ size_t domino_token_logprobs_workspace_size(int32_t batch, int32_t block, int32_
  * The weights carry both the mask and the normalisation (1 / number of live
  * positions, say); NULL stands for 1 / (batch * block) everywhere.  The loss
  * of a call without a live position is 0.
- * A position whose weight is 0 is not read, nor are its tokens, old_logp,
- * ref_logp and advantages; its logp, kl and gradient are 0.  A row of which
- * every logit is -inf has no distribution: logp -inf, kl 0, no loss, gradient
- * 0.  A live position whose token has probability 0 has an infinite kl where
- * ref_logp is given; with kl_coef != 0 its gradient is not finite.  A
- * live position whose logits hold NaN or +inf makes its own logp, kl and (unless
- * its advantage and kl_coef are 0) gradient and the loss NaN.
+ * The logits of a position whose weight is 0 are not read, and its token,
+ * old_logp, ref_logp and advantage are not used: all may hold anything.  Its
+ * logp, kl and gradient are 0.  A row of which every logit is -inf has no
+ * distribution: logp -inf, kl 0, no loss, gradient 0.  A live position whose
+ * token has probability 0 has an infinite kl where ref_logp is given (NaN where
+ * that is -inf too); with kl_coef != 0 its gradient is not finite.  A live
+ * position whose logits hold NaN or +inf makes its own logp, kl (where ref_logp
+ * is given) and (unless its advantage and kl_coef are 0) gradient and the loss
+ * NaN.
  *
  * logits      [batch, block, vocab] float32 (4-byte aligned)
  * tokens      [batch, block] int32; ids outside [0, vocab) are clamped
