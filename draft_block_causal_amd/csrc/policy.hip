@@ -53,9 +53,11 @@ namespace domino {
 constexpr int kPolThreads = 256;
 constexpr int kPolWaves = kPolThreads / 64;
 
-// log2(e) / T = hi + lo, hi of 16 bits, 2^-17 hi < lo (so that x = -inf stays -inf)
+// c = log2(e) / T, and c = hi + lo within 2^-40 of it, hi of 16 bits, 2^-17 hi < lo (so
+// that x = -inf stays -inf)
 struct Base2 {
   float hi, lo;
+  double c;
 };
 
 // Maximum of some logits (the exact one), and sums relative to R(m); the drafted
@@ -379,14 +381,18 @@ struct RowSum {
 __device__ __forceinline__ RowSum row_sum(SoftPart p, float x_y, Base2 c) {
   const float m = fmaxf(p.m, x_y);
   p = part_to(p, m, c);
-  const double c64 = (double)c.hi + (double)c.lo;  // as in the other terms: R may be large
-  const double t = far_out(m, c) ? ((double)x_y - (double)m) * c64 : fma((double)x_y, c64, -(double)ref_of(m, c));
+  const bool far = far_out(m, c);
+  // t with the other terms' hi + lo, as R may be large; what c has besides counts
+  // from the maximum on, where a token is far below it
+  const double pair = (double)c.hi + (double)c.lo, d = fmax((double)x_y - (double)m, -1e300);
+  const double t = far ? ((double)x_y - (double)m) * c.c : fma((double)x_y, pair, -(double)ref_of(m, c));
+  const double tc = far ? t : fma(c.c - pair, d, t);
   const double e = exp2(t), s = p.s + e;
   // -ln(1 + q), q = r / e, with what 1 + q rounds off put back (over 1 + q, to
   // first order); or ln 2 t - ln s
   const bool most = p.s < e;
   const double q = p.s / e, a = most ? 1.0 + q : s, l = log(a);
-  const double lp = most ? fma((a - 1.0) - q, 1.0 - q, -l) : fma(0.6931471805599453, t, -l);
+  const double lp = most ? fma((a - 1.0) - q, 1.0 - q, -l) : fma(0.6931471805599453, tc, -l);
   return RowSum{m, s, p.s, p.u, t, lp};
 }
 
@@ -398,8 +404,8 @@ __device__ __forceinline__ LogpOut logp_out(const SoftPart& p, float x_y, Base2 
   const RowSum q = row_sum(p, x_y, c);
   if (q.s == 0.0) return LogpOut{-INFINITY, 0.f};  // no distribution
   // ln s - ln 2 (u + e t) / s, in which what a token near 1 has of both cancels
-  // beforehand; e is 0 below
-  const double h = q.t > -4096.0 ? fma(0.6931471805599453, fma(q.t, q.r, -q.u) / q.s, -q.logp)
+  // beforehand; e counts for nothing below
+  const double h = q.t > -64.0 ? fma(0.6931471805599453, fma(q.t, q.r, -q.u) / q.s, -q.logp)
                                  : log(q.s) - 0.6931471805599453 * (q.u / q.s);
   return LogpOut{(float)q.logp, h < 0.0 ? 0.f : (float)h};
 }
@@ -883,7 +889,7 @@ static Base2 base2_factor(double temperature) {
     bits -= 0x100u;
     memcpy(&hi, &bits, 4);
   }
-  return Base2{hi, (float)(c - (double)hi)};
+  return Base2{hi, (float)(c - (double)hi), c};
 }
 
 template <bool ENT, bool ONCE>

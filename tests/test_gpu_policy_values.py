@@ -347,3 +347,30 @@ def test_token_of_no_probability_in_held_rows(dev):
         # tbar < 6.5 and rel(s) < 27 e; both losses, near -1, are rounded once
         assert abs((b - a).item() - 2 / rows) <= 2 / rows * 27 * E + 2 * E
         assert D.domino_policy_loss(x, y, lp, one, ref_logp=lp, kl_coef=0.1, grad=g).item() == np.inf
+
+
+@pytest.mark.parametrize("T", [0.7, 1.3, 60.3])
+@pytest.mark.parametrize("depth", [1e3, 1e5, 6e5, 1e7])
+def test_tokens_far_below_their_rows_maximum(dev, depth, T):
+    # log-probabilities of -1e3 ... -1e7: T counts with all its digits, so that a divergence from a reference near by is
+    # right to the bound of the row's sum
+    import draft_block_causal_amd as D
+
+    rng = np.random.default_rng(8)
+    for B, V in ((1, 300), (1, 40003), (34, 5003)):
+        x = (rng.normal(size=(B, 4, V)) * 2 * T).astype(np.float32)
+        y = rng.integers(0, V, size=(B, 4)).astype(np.int32)
+        np.put_along_axis(x, y[..., None].astype(np.int64), (-depth * T * rng.uniform(1, 2, (B, 4, 1))).astype(np.float32), -1)
+        x64 = x.astype(np.float64)
+        want, _ = O.token_logprobs(x, y, T)
+        ref = (want + rng.uniform(0.5, 1.5, want.shape)).astype(np.float32)
+        d = ref.astype(np.float64) - want
+        rel = _rel_s(x64, T) + 2.0**-50 * np.abs(want)  # (float64's own steps)
+        t = [torch.from_numpy(a).to(dev) for a in (x, y, want.astype(np.float32), np.ones(y.shape, np.float32), ref)]
+        kl, g = torch.full(y.shape, 99.0, device=dev), torch.empty_like(t[0])
+        for grad in (g, None):
+            D.domino_policy_loss(t[0], t[1], t[2], t[3], ref_logp=t[4], temperature=T, kl=kl, grad=grad)
+            got = kl.cpu().numpy().astype(np.float64)
+            value = np.expm1(d) - d
+            room = np.abs(np.expm1(d)) * 1.01 * rel + rel**2 + value * 1.01 * E
+            assert np.all(np.abs(got - value) <= room), (B, V, np.abs((got - value) / room).max())
