@@ -12,14 +12,14 @@
 // (With e among the sums grad_y was a difference of near equals: at 1 - p = 1e-6
 // off by a fifth of itself.)
 // R is an integer so that sums over different references are brought together
-// by exact factors; t_v is two fused products, with the first 16 bits of c and
-// with the rest, so it is off by about |t_v| 2^-23 at most.  Their roundings have
-// no preferred direction: with all 24 bits of a float32 in the first part, the
-// second product would be below half a step of most t_v and be lost (mean error
-// of a log-probability over 151936 entries at T = 1.2: 1.6e-8, 2e-9 so).
-// While |c M| < 2^20, the two roundings before R's own put R within 1/2 + 2^-3 of
-// c M, so the largest terms of s have |t_v| < 1.  (At 2^30 they were past what an
-// exponential can hold.)  A row outside (a mask value in every entry, say) is taken
+// by exact factors; t_v is two fused products, with the first 21 bits of c and
+// with the rest.  Their roundings have no preferred direction: with all 24 bits of a
+// float32 in the first part, the second product would be below half a step of most
+// t_v and be lost (mean error of a log-probability over 151936 entries at T = 1.2:
+// 1.6e-8, 1.4e-9 so).  While |c M| < 2^20, the second is below 1, so t_v is off by
+// (2 |t_v| + 1) 2^-24 at most, and the two roundings before R's own put R within
+// 1/2 + 2^-3 of c M, so the largest terms of s have |t_v| < 1.  (At 2^30 they were
+// past what an exponential can hold.)  A row outside (a mask value in every entry, say) is taken
 // again with t_v = c (x_v - M).
 // What a row has one of (ln s, the ratio, the divergence, the loss) is in
 // float64: a divergence is a small difference of numbers near 10.
@@ -53,8 +53,8 @@ namespace domino {
 constexpr int kPolThreads = 256;
 constexpr int kPolWaves = kPolThreads / 64;
 
-// c = log2(e) / T, and c = hi + lo within 2^-40 of it, hi of 16 bits, 2^-17 hi < lo (so
-// that x = -inf stays -inf)
+// c = log2(e) / T, and c = hi + lo within 2^-45 of it, hi of 21 bits, 2^-22 hi <= lo <
+// 2^-20 hi (so that x = -inf stays -inf)
 struct Base2 {
   float hi, lo;
   double c;
@@ -882,11 +882,11 @@ static Base2 base2_factor(double temperature) {
   const float f = (float)c;
   uint32_t bits;
   memcpy(&bits, &f, 4);
-  bits &= ~0xFFu;
+  bits &= ~7u;
   float hi;
   memcpy(&hi, &bits, 4);
-  if (c - (double)hi < (double)hi * 0x1p-17) {  // leave something for lo
-    bits -= 0x100u;
+  if (c - (double)hi < (double)hi * 0x1p-22) {  // leave something for lo
+    bits -= 8u;
     memcpy(&hi, &bits, 4);
   }
   return Base2{hi, (float)(c - (double)hi), c};

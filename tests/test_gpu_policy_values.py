@@ -374,3 +374,29 @@ def test_tokens_far_below_their_rows_maximum(dev, depth, T):
             value = np.expm1(d) - d
             room = np.abs(np.expm1(d)) * 1.01 * rel + rel**2 + value * 1.01 * E
             assert np.all(np.abs(got - value) <= room), (B, V, np.abs((got - value) / room).max())
+
+
+@pytest.mark.parametrize("T", [1.0, 0.83, 1.17, 0.59])
+@pytest.mark.parametrize("V", [2, 3])
+def test_single_terms_far_from_zero(dev, V, T):
+    # one or two terms besides the token's, so that no error averages out, up to and beyond the magnitude from which rows
+    # are taken around their maximum; the divergence at d = 1 shows the log-probability to 2e-8
+    import draft_block_causal_amd as D
+
+    rng = np.random.default_rng(V)
+    for log2 in (4, 10, 14, 16, 18, 19, 19.5, 19.9, 20.2, 22):
+        base = np.float32(2.0**log2 / LOG2E * T)
+        step = float(np.spacing(base)) if base > 2.0**17 else 2.0**-7
+        for sign in (1, -1):
+            x = (sign * base + step * np.round(rng.uniform(-6, 6, (64, 16, V)) / step)).astype(np.float32)
+            y = rng.integers(0, V, size=(64, 16)).astype(np.int32)
+            want, _ = O.token_logprobs(x, y, T)
+            ref = (want + 1).astype(np.float32)
+            d = ref.astype(np.float64) - want
+            t = [torch.from_numpy(a).to(dev) for a in (x, y, want.astype(np.float32), np.ones(y.shape, np.float32), ref)]
+            kl = torch.full(y.shape, 99.0, device=dev)
+            D.domino_policy_loss(t[0], t[1], t[2], t[3], ref_logp=t[4], temperature=T, kl=kl)
+            value = np.expm1(d) - d
+            rel = _rel_s(x.astype(np.float64), T)
+            err = np.abs(kl.cpu().numpy() - value) - value * 1.01 * E
+            assert np.all(err <= np.expm1(d) * 1.01 * rel + rel**2), (log2, sign, (err / np.expm1(d) / rel).max())
