@@ -13,14 +13,14 @@
 // off by a fifth of itself.)
 // R is an integer so that sums over different references are brought together
 // by exact factors; t_v is two fused products, with the first 21 bits of c and
-// with the rest.  Their roundings have no preferred direction: with all 24 bits of a
-// float32 in the first part, the second product would be below half a step of most
-// t_v and be lost (mean error of a log-probability over 151936 entries at T = 1.2:
-// 1.6e-8, 1.4e-9 so).  While |c M| < 2^20, the second is below 1, so t_v is off by
-// (2 |t_v| + 1) 2^-24 at most, and the two roundings before R's own put R within
-// 1/2 + 2^-3 of c M, so the largest terms of s have |t_v| < 1.  (At 2^30 they were
-// past what an exponential can hold.)  A row outside (a mask value in every entry, say) is taken
-// again with t_v = c (x_v - M).
+// with the rest.  Their roundings have no preferred direction: with all 24 bits of
+// a float32 in the first part, the second product would be below half a step of
+// most t_v and be lost (mean error of a log-probability over 151936 entries at
+// T = 1.2: 1.6e-8, 1.4e-9 so).  While |c M| < 2^20, the second product is below 1,
+// so t_v is off by (2 |t_v| + 1) 2^-24 at most, and the two roundings before R's
+// own put R within 1/2 + 2^-3 of c M, so the largest terms of s have |t_v| < 1.
+// (At 2^30 they were past what an exponential can hold.)  A row outside (a mask
+// value in every entry, say) is taken again with t_v = c (x_v - M).
 // What a row has one of (ln s, the ratio, the divergence, the loss) is in
 // float64: a divergence is a small difference of numbers near 10.
 //
